@@ -22,7 +22,8 @@ __all__ = ["MoeError", "MoeConfig", "MoeLayerWeights", "MoeLayer", "lib", "libra
            "moe_route", "moe_route_noalloc", "moe_forward", "moe_forward_host", "moe_destroy", "moe_debug_dequant", "moe_debug_last_routing", "moe_debug_bucket", "moe_check_status",
            "moe_get_stats", "moe_status_string", "moe_profile", "moe_profile_read", "moe_kernel_name", "MoeStats",
            "moe_debug_router_logits", "moe_router_error_depth", "moe_rms_normalize", "rms_normalize",
-           "moe_set_expert_range", "moe_debug_wait_limit"]
+           "moe_set_expert_range", "moe_debug_wait_limit", "MOE_OP_FP16", "MOE_OP_TRANSPOSE", "moe_check_op_status",
+           "grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmoe.so")
@@ -35,6 +36,8 @@ MOE_FORCE_UNFUSED = 0x10
 MOE_ROUTE_TAIL_SKIP = 0x20  # drop experts that every selecting token ranks >= MOE_TAIL_SKIP_RANK
 MOE_TAIL_SKIP_RANK = 6
 MOE_NORM_INPUT = 0x40  # the layer reads rmsnorm(x); with MOE_ACCUMULATE and y == x: x += layer(rmsnorm(x))
+MOE_OP_FP16 = 0x100  # 16-bit operators: operands and 16-bit results are fp16 (default: bf16)
+MOE_OP_TRANSPOSE = 0x200  # grouped product: multiply by W_e instead of its transpose
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_CUDA", 3: "MOE_ERR_OOM", 4: "MOE_ERR_NOT_LOADED",
           5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_BOUNDS", 7: "MOE_ERR_RANGE"}
 
@@ -118,6 +121,17 @@ def lib() -> ctypes.CDLL:
             L.moe_set_expert_range.argtypes = [vp, i32, i32, i32]
             L.moe_debug_wait_limit.restype = st
             L.moe_debug_wait_limit.argtypes = [vp, u32, i32]
+            i64 = ctypes.c_int64
+            L.moe_grouped_matmul.restype = st
+            L.moe_grouped_matmul.argtypes = [vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, u32, vp]
+            L.moe_grouped_wgrad.restype = st
+            L.moe_grouped_wgrad.argtypes = [vp, i64, vp, i64, i32, vp, i32, i32, i32, vp, u32, vp]
+            L.moe_swiglu.restype = st
+            L.moe_swiglu.argtypes = [vp, i64, i32, i32, vp, vp, vp, i64, u32, vp]
+            L.moe_swiglu_backward.restype = st
+            L.moe_swiglu_backward.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp, u32, vp]
+            L.moe_check_op_status.restype = st
+            L.moe_check_op_status.argtypes = []
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [st]
             _lib = L
@@ -209,6 +223,11 @@ def moe_rms_normalize(x_ptr: int, T: int, d: int, out_ptr: int, stream: int) -> 
 
 def moe_check_status(handle: int) -> int:
     return int(lib().moe_check_status(handle))
+
+
+def moe_check_op_status() -> int:
+    """Synchronise the current device; the first device-side error of the handle-free operators, then cleared."""
+    return int(lib().moe_check_op_status())
 
 
 def moe_get_stats(handle: int):
@@ -365,3 +384,13 @@ class MoeLayer:
             self.close()
         except Exception:
             pass
+
+
+def __getattr__(name):
+    # the 16-bit operators work on torch tensors: their module imports torch, so it loads on first use
+    if name in ("grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward"):
+        from . import experts16
+        fn = getattr(experts16, name)
+        globals()[name] = fn
+        return fn
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

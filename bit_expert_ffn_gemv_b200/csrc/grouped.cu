@@ -1,0 +1,501 @@
+// grouped.cu -- matrix products of ragged row groups with 16-bit matrices
+// (tcgen05, pairs of SMs), and their gradients.
+//
+// Group e owns rows o[e] <= r < o[e+1] and a matrix W_e [N x K]:
+//   forward   y[r, n]    = sum_k x[r, k] W_e[n, k]
+//   rows      dx[r, k]   = sum_n dy[r, n] W_e[n, k]
+//   weights   dW_e[n, k] = sum_r dy[r, n] x[r, k]
+// The unquantised counterpart of the expert GEMMs of gemm_sm100.cu: the
+// products a token's selected experts are (tech.okbari.net guide, section
+// "Strata, Qwen and GSQ-RCO are different components").
+//
+// One tile is 256 features by up to 256 columns, held by a cluster of two CTAs
+// (cta_group::2, M = 256): each CTA stages its own 128 features and half of the
+// columns' operand, which halves the column operand's shared-memory traffic per
+// SM against one-SM tiles.  For the forward and rows products the features are
+// the MMA's M and the group's rows its N (rounded up to 32): a group of few
+// rows costs few columns, not a padded 128-row tile.  For the weight gradient
+// M is n, N is k and the contraction runs over the group's rows; both operands
+// are read MN-major, straight from row-major memory.
+//
+// Warp roles (every role walks the same tile sequence; persistent):
+//   warp 0      loader (one thread): TMA of this CTA's halves into a 6-deep
+//               ring of K = 64 steps, completing on the leader's full[stage]
+//   warp 1      MMA issuer (leader CTA, one thread)
+//   warp 2      tensor-memory allocation; weight gradient: zeroes the rows of
+//               the last step that belong to the next group (a product with
+//               zero would let their infinities and NaN through, so both
+//               operands are cleared)
+//   warps 4-7   epilogue: TMEM -> registers -> shared transpose -> 16-byte
+//               stores; two accumulators, so it overlaps the next tile's MMAs
+// Every wait is bounded.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace moe {
+
+constexpr int kGroupedThreads = 256;
+constexpr int kGroupedStages = 6;
+constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an operand, one K = 64 step
+constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
+constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
+constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
+constexpr int kGroupedSmem = kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + 1024;
+constexpr int kGroupedMaxGroups = 1024;
+// fp32 results: the tensor core rounds its accumulator towards zero at every
+// 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
+// relative after 1875 steps), so the contraction is cut into parts of this
+// many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
+// by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
+constexpr int kPartSteps = 8;
+static_assert(kGroupedSmem + 8 * (kGroupedMaxGroups + 8) <= 227 * 1024, "shared memory");
+
+struct GroupedMaps {
+    CUtensorMap a, b, b_small;
+};
+
+// 16-bit pair in the requested type
+MOE_DEV uint32_t pack16(float lo, float hi, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+MOE_DEV uint16_t to16(float v, bool bf16) {
+    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// four fp32 values at p, or added to those there (the same thread wrote them)
+MOE_DEV void add_store(float* p, const uint4& v, bool add) {
+    float4 s = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    if (add) {
+        const float4 was = *reinterpret_cast<const float4*>(p);
+        s = make_float4(was.x + s.x, was.y + s.y, was.z + s.z, was.w + s.w);
+    }
+    *reinterpret_cast<float4*>(p) = s;
+}
+
+struct GroupedTile {
+    int e, row0, n;  // group; first row and rows of the tile (weights: of the group)
+    int f0, g0;      // first feature (of the pair); weights: first k column
+};
+
+// The tile list: forward and rows products enumerate (group, 256-row block)
+// by a prefix sum over the groups, features innermost, so the CTAs that run
+// together share the group's rows and its matrix through L2.
+template <int MODE>
+MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int64_t t, const int* start, const int* pre, int JT) {
+    GroupedTile r;
+    if (MODE == kGroupedWeights) {
+        const int per = JT * ((g.C + 255) >> 8);
+        r.e = (int)(t / per);
+        const int in = (int)(t - (int64_t)r.e * per);
+        r.f0 = (in % JT) << 8;
+        r.g0 = (in / JT) << 8;
+        r.row0 = start[r.e];
+        r.n = pre[r.e];
+        return r;
+    }
+    const int q = (int)(t / JT);
+    r.f0 = (int)(t - (int64_t)q * JT) << 8;
+    r.g0 = 0;
+    int lo = 0, hi = g.E - 1;  // last group with pre <= q
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= q) lo = mid;
+        else hi = mid - 1;
+    }
+    r.e = lo;
+    const int first = start[lo] + ((q - pre[lo]) << 8);
+    r.row0 = first;
+    r.n = min(256, start[lo + 1] - first);
+    return r;
+}
+
+template <int MODE, bool OUT32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
+    grouped_kernel(const GroupedArgs g, const __grid_constant__ CUtensorMap amap,
+                   const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap bmap_s) {
+    constexpr bool WG = MODE == kGroupedWeights;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[kGroupedStages], empty_bar[kGroupedStages], tail_bar[kGroupedStages];
+    __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int start[kGroupedMaxGroups + 1], pre[kGroupedMaxGroups + 1];
+    __shared__ int wsum[kGroupedThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t rank = tc::cta_rank();
+    const int JT = (g.F + 255) >> 8;
+
+    if (tid == 0) {
+        for (int i = 0; i < kGroupedStages; ++i) {
+            mbar_init(&full_bar[i], 2);
+            mbar_init(&empty_bar[i], 1);
+            mbar_init(&tail_bar[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf_bar[i], 1);
+            mbar_init(&acce_bar[i], 8);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tc::tmem_alloc_pair(&tmem_slot, 512);
+
+    // group starts, clamped into [0, M] and kept ascending (a bad table reads
+    // and writes nothing out of range); pre = prefix sum of the groups' row
+    // blocks, or (weights) each group's row count
+    for (int i = tid; i <= g.E; i += kGroupedThreads) start[i] = min(max(__ldg(&g.offsets[i]), 0), g.M);
+    __syncthreads();
+    constexpr int kPer = (kGroupedMaxGroups + kGroupedThreads - 1) / kGroupedThreads;
+    int blocks[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        const int c = e < g.E ? max(start[e + 1] - start[e], 0) : 0;
+        if (WG && e < g.E) pre[e] = c;
+        blocks[i] = (c + 255) >> 8;
+        mine += blocks[i];
+    }
+    int64_t total;
+    if (WG) {
+        total = (int64_t)g.E * JT * ((g.C + 255) >> 8);
+    } else {
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int before = inc - mine, all = 0;
+#pragma unroll
+        for (int w = 0; w < kGroupedThreads / 32; ++w) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i;
+            if (e < g.E) pre[e] = before;
+            before += blocks[i];
+        }
+        total = (int64_t)all * JT;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();  // both CTAs' barriers are initialised, both halves of tensor memory allocated
+    tc::fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+    const int KC = (g.C + 63) >> 6;  // steps per tile (forward, rows)
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ======================= loader
+            bool ok = true;
+            int j = 0;
+            uint32_t full_leader[kGroupedStages];
+#pragma unroll
+            for (int i = 0; i < kGroupedStages; ++i) full_leader[i] = tc::cluster_addr(&full_bar[i], 0);
+            for (int64_t t = pair; t < total && ok; t += pairs) {
+                const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+                const int KS = WG ? (tl.n + 63) >> 6 : KC;
+                const int nh = WG ? 128 : ((tl.n + 31) & ~31) >> 1;
+                const int brow = tl.row0 + (int)rank * nh;
+                const int f = tl.f0 + (int)rank * 128;
+                const int nbox = nh > 64 ? 0 : (nh + 31) >> 5;  // 32-row boxes (0: one of 128 rows)
+                const uint32_t bytes = kHalfTile + (WG || nbox == 0 ? kHalfTile : nbox * 32 * 128);
+                for (int s = 0; s < KS; ++s, ++j) {
+                    const int st = j % kGroupedStages;
+                    if (j >= kGroupedStages) ok = tc::bar_wait_cluster(&empty_bar[st], ((j / kGroupedStages) - 1) & 1, g.status);
+                    if (!ok) break;
+                    uint8_t* As = smem + st * kGroupedStage;
+                    uint8_t* Bs = As + kHalfTile;
+                    // a last step that ends inside 16 rows is completed by warp 2 once it is cleared
+                    const bool tail = WG && s == KS - 1 && (tl.n & 15);
+                    uint32_t bar;
+                    if (tail) {
+                        mbar_arrive_expect_tx(&tail_bar[st], bytes);
+                        bar = tc::cluster_addr(&tail_bar[st], rank);
+                    } else {
+                        bar = full_leader[0] + (uint32_t)st * 8u;
+                        tc::arrive_expect_cluster(bar, bytes);
+                    }
+                    if (WG) {
+                        const int r = tl.row0 + s * 64;
+                        tc::tma_2d_pair(As, &amap, f, r, bar);
+                        tc::tma_2d_pair(As + kPanel, &amap, f + 64, r, bar);
+                        tc::tma_2d_pair(Bs, &bmap, tl.g0 + (int)rank * 128, r, bar);
+                        tc::tma_2d_pair(Bs + kPanel, &bmap, tl.g0 + (int)rank * 128 + 64, r, bar);
+                    } else {
+                        if (MODE == kGroupedForward) {
+                            tc::tma_3d_pair(As, &amap, s * 64, f, tl.e, bar);
+                        } else {
+                            tc::tma_3d_pair(As, &amap, f, s * 64, tl.e, bar);
+                            tc::tma_3d_pair(As + kPanel, &amap, f + 64, s * 64, tl.e, bar);
+                        }
+                        if (nbox == 0) tc::tma_2d_pair(Bs, &bmap, s * 64, brow, bar);
+                        else
+                            for (int i = 0; i < nbox; ++i)
+                                tc::tma_2d_pair(Bs + i * 32 * 128, &bmap_s, s * 64, brow + i * 32, bar);
+                    }
+                }
+            }
+            if (!ok) tc::settle();
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            // ======================= MMA issuer
+            bool ok = true;
+            int j = 0, it = 0;
+            for (int64_t t = pair; t < total && ok; t += pairs) {
+                const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+                const int KS = WG ? (tl.n + 63) >> 6 : KC;
+                const uint32_t idesc = tc::idesc_f16_major(256, WG ? 256 : (tl.n + 31) & ~31, g.bf16 != 0,
+                                                           MODE != kGroupedForward, WG);
+                for (int s = 0; s < KS; ++s, ++j) {
+                    const int st = j % kGroupedStages, ps = OUT32 ? s % kPartSteps : s;
+                    if (ps == 0) {  // a new part: the next accumulator, once the epilogue has drained it
+                        if (it > 1) ok = tc::bar_wait_cluster(&acce_bar[it & 1], ((it >> 1) - 1) & 1, g.status);
+                        if (!ok) break;
+                        tc::fence_after();
+                    }
+                    const uint32_t acc_addr = tmem + (it & 1) * 256;
+                    ok = tc::bar_wait_cluster(&full_bar[st], (j / kGroupedStages) & 1, g.status);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t a_addr = smem_addr(smem + st * kGroupedStage), b_addr = a_addr + kHalfTile;
+                    const int kks = WG && s == KS - 1 ? (tl.n - s * 64 + 15) >> 4 : 4;
+                    for (int kk = 0; kk < kks; ++kk) {
+                        const uint64_t ad = MODE == kGroupedForward ? tc::sdesc(a_addr + kk * 32)
+                                                                    : tc::sdesc_mn(a_addr + kk * 2048, kPanel);
+                        const uint64_t bd = WG ? tc::sdesc_mn(b_addr + kk * 2048, kPanel) : tc::sdesc(b_addr + kk * 32);
+                        tc::mma_pair(acc_addr, ad, bd, idesc, (ps > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::commit_pair(&empty_bar[st]);
+                    if (s == KS - 1 || (OUT32 && ps == kPartSteps - 1)) tc::commit_pair(&accf_bar[it++ & 1]);
+                }
+            }
+            if (!ok) tc::settle();
+        }
+    } else if (WG && warp == 2) {
+        // ======================= rows of a group's last step that are not its own
+        bool ok = true;
+        int j = 0;
+        uint32_t phases = 0;  // per stage: parity of its next cleared step
+        for (int64_t t = pair; t < total && ok; t += pairs) {
+            const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+            const int KS = (tl.n + 63) >> 6;
+            j += KS;
+            if (!(tl.n & 15)) continue;
+            const int st = (j - 1) % kGroupedStages;
+            ok = true;
+            if (lane == 0) ok = tc::bar_wait_cluster(&tail_bar[st], (phases >> st) & 1, g.status);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            phases ^= 1u << st;
+            const int r0 = tl.n - (KS - 1) * 64, nz = ((r0 + 15) & ~15) - r0;
+            uint8_t* base = smem + st * kGroupedStage + r0 * 128;
+            for (int i = lane; i < 4 * nz * 8; i += 32) {
+                const int p = i / (nz * 8), c = i - p * nz * 8;
+                *reinterpret_cast<uint4*>(base + p * kPanel + c * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&full_bar[st], 0));
+        }
+    } else if (warp >= 4) {
+        // ======================= epilogue: lane = feature, register = column
+        const int q = warp & 3;
+        uint8_t* stg = smem + kGroupedStages * kGroupedStage + q * kEpiWarpBytes;
+        bool ok = true;
+        int it = 0;
+        const bool bf16 = g.bf16 != 0;
+        for (int64_t t = pair; t < total && ok; t += pairs) {
+            const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+            const bool empty = WG && tl.n == 0;
+            if (empty && g.accumulate) continue;
+            const int KS = WG ? (tl.n + 63) >> 6 : KC;
+            const int parts = OUT32 && !empty ? (KS + kPartSteps - 1) / kPartSteps : 1;
+            for (int part = 0; part < parts; ++part) {
+                const int b = it & 1, use = it >> 1;
+                const bool add = OUT32 && (part > 0 || g.accumulate);
+                if (!empty) {
+                    ++it;
+                    if (lane == 0) ok = tc::bar_wait_cluster(&accf_bar[b], use & 1, g.status);
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    tc::fence_after();
+                }
+                const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + b * 256;
+                const int f = tl.f0 + (int)rank * 128 + 32 * q;  // the warp's first feature
+                if (!WG) {
+                    // 16 rows at a time: [row][32 features] in shared memory, then whole 16-byte pieces of the rows
+                    constexpr int kVec = OUT32 ? 4 : 8, kSegs = 32 / kVec, kRowsPer = 32 / kSegs;
+                    const int seg = lane % kSegs, vr = lane / kSegs;
+                    const bool in = f + seg * kVec < g.F;
+                    const int64_t at = (int64_t)tl.row0 * g.ldo + f + seg * kVec;
+                    uint32_t r[16];
+                    tc::ld16_nowait(tb, r);
+                    tc::ld_wait();
+                    for (int c0 = 0; c0 < tl.n; c0 += 16) {
+                        if (OUT32) {
+    #pragma unroll
+                            for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(stg)[i * 32 + lane] = r[i];
+                        } else {
+    #pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                reinterpret_cast<uint16_t*>(stg)[i * 32 + lane] = to16(__uint_as_float(r[i]), bf16);
+                        }
+                        const bool more = c0 + 16 < tl.n;
+                        if (more) tc::ld16_nowait(tb + c0 + 16, r);
+                        __syncwarp();
+    #pragma unroll
+                        for (int p = 0; p < 16 / kRowsPer; ++p) {
+                            const int row = p * kRowsPer + vr;
+                            if (in && c0 + row < tl.n) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(stg + row * (OUT32 ? 128 : 64) + seg * 16);
+                                const int64_t o = at + (int64_t)(c0 + row) * g.ldo;
+                                if (OUT32) add_store(static_cast<float*>(g.out) + o, v, add);
+                                else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + o) = v;
+                            }
+                        }
+                        __syncwarp();
+                        if (more) tc::ld_wait();
+                    }
+                } else {
+                    // 128 bytes of each of the warp's 32 rows at a time, 16-byte pieces permuted against bank conflicts
+                    constexpr int kCols = OUT32 ? 32 : 64, kVec = OUT32 ? 4 : 8;
+                    for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
+                        if (empty) {
+    #pragma unroll
+                            for (int p = 0; p < 8; ++p)
+                                *reinterpret_cast<uint4*>(stg + lane * 128 + p * 16) = make_uint4(0, 0, 0, 0);
+                        } else {
+    #pragma unroll
+                            for (int h = 0; h < kCols; h += 32) {
+                                uint32_t r[32];
+                                tc::ld16_nowait(tb + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                                tc::ld16_nowait(tb + c0 + h + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                                tc::ld_wait();
+    #pragma unroll
+                                for (int p = 0; p < 32 / kVec; ++p) {
+                                    uint4 v;
+                                    if (OUT32) {
+                                        v = make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
+                                    } else {
+                                        uint32_t w[4];
+    #pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            w[i] = pack16(__uint_as_float(r[(8 * p + 2 * i) & 31]),
+                                                          __uint_as_float(r[(8 * p + 2 * i + 1) & 31]), bf16);
+                                        v = make_uint4(w[0], w[1], w[2], w[3]);
+                                    }
+                                    const int piece = h / kVec + p;
+                                    *reinterpret_cast<uint4*>(stg + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        const int col = tl.g0 + c0 + (lane & 7) * kVec;
+    #pragma unroll
+                        for (int p = 0; p < 8; ++p) {
+                            const int row = p * 4 + (lane >> 3);
+                            if (f + row < g.F && col < g.C) {
+                                uint4 v = *reinterpret_cast<const uint4*>(stg + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                                const int64_t o = ((int64_t)tl.e * g.F + f + row) * g.ldo + col;
+                                if (OUT32) {
+                                    add_store(static_cast<float*>(g.out) + o, v, add);
+                                } else {
+                                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + o) = v;
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (!empty) {
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&acce_bar[b], 0));
+                }
+            }
+        }
+        if (!ok) tc::settle();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();  // neither CTA leaves while the other may still signal it or read its operands
+    tc::fence_after();
+    if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------- launcher
+static int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    return sms;
+}
+
+// map of a row-major 16-bit matrix [rows x cols], rows `ld` values apart; boxes of 64 columns x box_rows
+static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                          int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, str[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    return encode_sw128(m, bf16, base, 2, dims, str, box);
+}
+
+template <int MODE, bool OUT32>
+static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
+    auto kern = grouped_kernel<MODE, OUT32>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGroupedSmem);
+    if (e != cudaSuccess) return e;
+    const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
+    kern<<<2 * pairs, kGroupedThreads, kGroupedSmem, s>>>(g, m.a, m.b, m.b_small);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const void* x, int64_t ldx, const void* dy,
+                           int64_t lddy, bool out_fp32, cudaStream_t s) {
+    GroupedMaps m{};
+    const bool bf = g.bf16 != 0;
+    cudaError_t e;
+    const int JT = (g.F + 255) / 256;
+    if (mode == kGroupedWeights) {
+        e = map_2d(&m.a, bf, dy, g.M, g.F, lddy, 64);
+        if (e == cudaSuccess) e = map_2d(&m.b, bf, x, g.M, g.C, ldx, 64);
+        if (e != cudaSuccess) return e;
+        m.b_small = m.b;
+        const int64_t tiles = (int64_t)g.E * JT * ((g.C + 255) / 256);
+        return out_fp32 ? grouped_launch<kGroupedWeights, true>(g, m, tiles, s)
+                        : grouped_launch<kGroupedWeights, false>(g, m, tiles, s);
+    }
+    // W as [E][N][K]: the features are its rows (forward) or its columns (rows gradient)
+    const int N = mode == kGroupedForward ? g.F : g.C, K = mode == kGroupedForward ? g.C : g.F;
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)g.E};
+    const cuuint64_t str[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
+    const cuuint32_t box[3] = {64, mode == kGroupedForward ? 128u : 64u, 1};
+    e = encode_sw128(&m.a, bf, w, 3, dims, str, box);
+    const void* rows = mode == kGroupedForward ? x : dy;
+    const int64_t ld = mode == kGroupedForward ? ldx : lddy;
+    if (e == cudaSuccess) e = map_2d(&m.b, bf, rows, g.M, g.C, ld, 128);
+    if (e == cudaSuccess) e = map_2d(&m.b_small, bf, rows, g.M, g.C, ld, 32);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((int64_t)(g.M + 255) / 256 + (g.E < g.M ? g.E : g.M)) * JT;
+    if (mode == kGroupedForward)
+        return out_fp32 ? grouped_launch<kGroupedForward, true>(g, m, tiles, s)
+                        : grouped_launch<kGroupedForward, false>(g, m, tiles, s);
+    return out_fp32 ? grouped_launch<kGroupedRows, true>(g, m, tiles, s)
+                    : grouped_launch<kGroupedRows, false>(g, m, tiles, s);
+}
+
+}  // namespace moe

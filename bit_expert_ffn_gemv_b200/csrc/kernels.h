@@ -158,7 +158,44 @@ cudaError_t launch_gemm_down(const ExpertArgs& a, const GemmMaps& maps, const fl
                              const int4* desc, const int32_t* counts, cudaStream_t s);
 cudaError_t launch_combine_f16(const CombineArgs& a, const void* o, cudaStream_t s);
 cudaError_t launch_rms_normalize(const void* x, int T, int d, void* out, float eps, cudaStream_t s);
+// a tensor map of a 16-bit row-major tensor (rank 2 or 3), 128-byte swizzle, values outside read as zeros
+cudaError_t encode_sw128(CUtensorMap* map, bool bf16, const void* base, int rank, const cuuint64_t* dims,
+                         const cuuint64_t* strides_bytes, const cuuint32_t* box);
 cudaError_t launch_dequant(const uint8_t* codes, const uint16_t* scales, int N, int K, int bits, float* out,
                            cudaStream_t s);
+
+// ---------------------------------------------------------------- 16-bit experts: grouped products
+// Modes of the grouped product: y = x W^T, dx = dy W, dW = dy^T x.
+constexpr int kGroupedForward = 0, kGroupedRows = 1, kGroupedWeights = 2;
+struct GroupedArgs {
+    const int32_t* offsets;  // [E + 1] row ranges of the groups
+    int E, M;                // groups; rows of the row matrices
+    int F;                   // features: N (forward, weights) or K (rows)
+    int C;                   // forward: K, rows: N (the contraction); weights: K (the result's columns)
+    void* out;
+    int64_t ldo;             // row pitch of out in values (weights: K)
+    int bf16;                // operands (and a 16-bit out) are bf16, else fp16
+    int accumulate;          // weights, fp32 out: add to out
+    uint32_t* status;
+};
+cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const void* x, int64_t ldx, const void* dy,
+                           int64_t lddy, bool out_fp32, cudaStream_t s);
+
+// SwiGLU between an expert's products, and its gradient (dh, dgu, drw).
+struct SwigluArgs {
+    const void* gu;       // [M x 2f] gate values, then up values
+    int64_t ldgu;
+    int M, f;
+    const float* rw;      // [M] row weights or null
+    const int32_t* n_rows;  // device: rows in use (<= M), or null
+    void* h;              // [M x f] (gradient: or null)
+    int64_t ldh;
+    const void* dh;
+    int64_t lddh;
+    void* dgu;
+    int64_t lddgu;
+    float* drw;           // [M] or null
+};
+cudaError_t launch_swiglu(const SwigluArgs& a, bool bf16, bool grad, cudaStream_t s);
 
 }  // namespace moe

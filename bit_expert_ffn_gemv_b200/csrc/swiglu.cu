@@ -1,0 +1,145 @@
+// swiglu.cu -- the activation between an expert's two products, and its gradient.
+//
+//   h   = rw * g s u                      s = 1 / (1 + e^-g), gu = [g | u] per row
+//   dg  = rw * dh u s (1 + g (1 - s))     du = rw * dh g s
+//   drw = sum_j dh_j g_j s_j u_j          (the routing weight's gradient)
+// rw: an optional fp32 weight per row (a token's routing weight, folded into h
+// so that the down product needs no epilogue and its gradient stays local).
+//
+// Bound by HBM: every value is read once and written once, 16 bytes per lane;
+// a row's loads are all issued before its arithmetic.  One warp owns a row
+// when there are enough rows to fill the GPU (drw is then a shuffle), eight
+// warps share one otherwise.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+template <bool BF16>
+MOE_DEV void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        } else {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            f[2 * i] = p.x;
+            f[2 * i + 1] = p.y;
+        }
+    }
+}
+template <bool BF16>
+MOE_DEV uint4 pack8(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&p);
+        } else {
+            const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+MOE_DEV float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+constexpr int kSwigluThreads = 256;
+constexpr int kSwigluFewRows = 148 * 8 * 4;  // below this many rows a whole block takes each row
+
+template <bool BF16, int WARPS>
+__global__ void __launch_bounds__(kSwigluThreads) swiglu_kernel(const SwigluArgs a) {
+    const int per = 8 / WARPS, lanes = WARPS * 32;
+    const int r = blockIdx.x * per + (WARPS == 1 ? threadIdx.x >> 5 : 0);
+    const int lane = threadIdx.x & (lanes - 1);
+    const int rows = a.n_rows ? min(__ldg(a.n_rows), a.M) : a.M;
+    if (r >= rows) return;
+    const uint16_t* gu = static_cast<const uint16_t*>(a.gu) + (int64_t)r * a.ldgu;
+    uint16_t* h = static_cast<uint16_t*>(a.h) + (int64_t)r * a.ldh;
+    const float rw = a.rw ? __ldg(&a.rw[r]) : 1.0f;
+#pragma unroll 4
+    for (int c = lane * 8; c < a.f; c += lanes * 8) {
+        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(gu + c));
+        const uint4 uv = __ldg(reinterpret_cast<const uint4*>(gu + a.f + c));
+        float g[8], u[8];
+        unpack8<BF16>(gv, g);
+        unpack8<BF16>(uv, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = rw * (g[i] * sigmoid(g[i]) * u[i]);
+        *reinterpret_cast<uint4*>(h + c) = pack8<BF16>(g);
+    }
+}
+
+template <bool BF16, int WARPS>
+__global__ void __launch_bounds__(kSwigluThreads) swiglu_grad_kernel(const SwigluArgs a) {
+    __shared__ float part[8];
+    const int per = 8 / WARPS, lanes = WARPS * 32;
+    const int r = blockIdx.x * per + (WARPS == 1 ? threadIdx.x >> 5 : 0);
+    const int lane = threadIdx.x & (lanes - 1);
+    const int rows = a.n_rows ? min(__ldg(a.n_rows), a.M) : a.M;
+    if (r >= rows) return;  // the whole warp, and with eight warps per row the whole block
+    const uint16_t* gu = static_cast<const uint16_t*>(a.gu) + (int64_t)r * a.ldgu;
+    const uint16_t* dhp = static_cast<const uint16_t*>(a.dh) + (int64_t)r * a.lddh;
+    uint16_t* dgu = static_cast<uint16_t*>(a.dgu) + (int64_t)r * a.lddgu;
+    uint16_t* h = a.h ? static_cast<uint16_t*>(a.h) + (int64_t)r * a.ldh : nullptr;
+    const float rw = a.rw ? __ldg(&a.rw[r]) : 1.0f;
+    float dot = 0.f;
+#pragma unroll 4
+    for (int c = lane * 8; c < a.f; c += lanes * 8) {
+        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(gu + c));
+        const uint4 uv = __ldg(reinterpret_cast<const uint4*>(gu + a.f + c));
+        const uint4 dv = __ldg(reinterpret_cast<const uint4*>(dhp + c));
+        float g[8], u[8], d[8], hh[8];
+        unpack8<BF16>(gv, g);
+        unpack8<BF16>(uv, u);
+        unpack8<BF16>(dv, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float s = sigmoid(g[i]), act = g[i] * s, act_u = act * u[i], dw = rw * d[i];
+            hh[i] = rw * act_u;
+            dot = fmaf(d[i], act_u, dot);
+            g[i] = dw * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+            u[i] = dw * act;
+        }
+        *reinterpret_cast<uint4*>(dgu + c) = pack8<BF16>(g);
+        *reinterpret_cast<uint4*>(dgu + a.f + c) = pack8<BF16>(u);
+        if (h) *reinterpret_cast<uint4*>(h + c) = pack8<BF16>(hh);
+    }
+    if (!a.drw) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+        __syncthreads();
+        dot = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) dot += part[w];
+    }
+    if (lane == 0) a.drw[r] = dot;
+}
+
+template <bool BF16>
+static void launch(const SwigluArgs& a, bool grad, cudaStream_t s) {
+    const bool few = a.M < kSwigluFewRows;
+    const int blocks = few ? a.M : (a.M + 7) / 8;
+    if (grad) {
+        if (few) swiglu_grad_kernel<BF16, 8><<<blocks, kSwigluThreads, 0, s>>>(a);
+        else swiglu_grad_kernel<BF16, 1><<<blocks, kSwigluThreads, 0, s>>>(a);
+    } else {
+        if (few) swiglu_kernel<BF16, 8><<<blocks, kSwigluThreads, 0, s>>>(a);
+        else swiglu_kernel<BF16, 1><<<blocks, kSwigluThreads, 0, s>>>(a);
+    }
+}
+
+cudaError_t launch_swiglu(const SwigluArgs& a, bool bf16, bool grad, cudaStream_t s) {
+    if (bf16) launch<true>(a, grad, s);
+    else launch<false>(a, grad, s);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

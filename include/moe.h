@@ -388,6 +388,86 @@ moe_status moe_profile_read(moe_handle* h, double* total_ms, int64_t* launches);
 /* Static name of kernel id i ("unknown" when out of range). */
 const char* moe_kernel_name(int32_t kernel);
 
+/*
+ * ---- 16-bit experts: grouped products, SwiGLU ----
+ *
+ * The expert FFN with unquantised (bf16 or fp16) matrices, and its gradients:
+ * the products o_e = W_d,e (silu(W_g,e x) * W_u,e x) of the same layer (tech.
+ * okbari.net guide, section "Strata, Qwen and GSQ-RCO are different
+ * components"), for experts that are not, or not yet, quantised, and for
+ * tuning them.  Rows are (token, expert) pairs sorted by expert, as the
+ * grouping step orders them (moe_debug_bucket's offsets).
+ *
+ * Conventions of these calls
+ *   - No handle and no device allocation: the buffers are the caller's, and
+ *     calls on different streams are independent.  Any call may be captured in
+ *     a CUDA graph (after one call outside a capture has loaded the module).
+ *   - All tensors are on the current device, 16-byte aligned (offsets and fp32
+ *     vectors: 4 bytes).  Matrices are row-major; ld* is a row pitch in
+ *     values, a multiple of 8.  Column counts are multiples of 8.
+ *   - Operands and 16-bit results are bf16, or fp16 with MOE_OP_FP16.  Every
+ *     sum is held in fp32 and rounded once.
+ *   - offsets [n_groups + 1] (device, int32, ascending) give the groups' row
+ *     ranges; rows before offsets[0] and from offsets[n_groups] on belong to
+ *     no group: they are not read into any result, and their result rows are
+ *     left as they were.  Values are clamped to [0, rows].
+ *   - rows = 0 is valid.  A device-side wait that ran out surfaces through
+ *     moe_check_op_status.
+ */
+#define MOE_OP_FP16 0x100u      /* operands and 16-bit results are fp16 (default: bf16) */
+#define MOE_OP_TRANSPOSE 0x200u /* multiply by W_e instead of its transpose */
+
+/*
+ * y[r] = W_e x[r] for every row r of every group e: x [rows x k], w [n_groups x
+ * n x k] contiguous, y [rows x n].  With MOE_OP_TRANSPOSE y[r] = W_e^T x[r]: x
+ * [rows x n], y [rows x k] -- the gradient of the forward product's rows.  y
+ * is 16-bit, or fp32 with MOE_OUT_FP32, and overlaps no operand.
+ * Errors: INVALID_ARG (rows outside [0, 2^27], n_groups outside [1, 1024], n
+ * or k not a multiple of 8 or above 2^17, a pitch that is short or no multiple
+ * of 8, NULL or misaligned pointer, unknown flag), CUDA.
+ */
+moe_status moe_grouped_matmul(const void* x, int64_t ldx, int32_t rows, const void* w, const int32_t* offsets,
+                              int32_t n_groups, int32_t n, int32_t k, void* y, int64_t ldy, uint32_t flags,
+                              void* stream);
+
+/*
+ * dw[e] = sum over the rows r of group e of dy[r]^T x[r]: dy [rows x n], x [rows
+ * x k], dw [n_groups x n x k] contiguous, 16-bit, or fp32 with MOE_OUT_FP32; with
+ * MOE_ACCUMULATE (fp32 only) dw is added to.  An empty group's matrix is zeros
+ * (accumulating: left as it was).  Errors: as moe_grouped_matmul, and
+ * INVALID_ARG for MOE_ACCUMULATE without MOE_OUT_FP32.
+ */
+moe_status moe_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, int32_t rows,
+                             const int32_t* offsets, int32_t n_groups, int32_t n, int32_t k, void* dw,
+                             uint32_t flags, void* stream);
+
+/*
+ * h[r] = row_weights[r] * silu(g[r]) * u[r] with gu [rows x 2f] = [g | u] (the
+ * product with an expert's gate rows followed by its up rows), h [rows x f].
+ * row_weights (fp32 [rows]) may be NULL (1).  n_rows (device int32) may be NULL;
+ * otherwise rows from *n_rows on are left as they were (pass offsets + n_groups).
+ * Errors: INVALID_ARG, CUDA.
+ */
+moe_status moe_swiglu(const void* gu, int64_t ldgu, int32_t rows, int32_t f, const float* row_weights,
+                      const int32_t* n_rows, void* h, int64_t ldh, uint32_t flags, void* stream);
+
+/*
+ * Gradient of moe_swiglu for dh [rows x f]: dgu [rows x 2f]; h [rows x f] (the
+ * forward's result again, for the down matrices' gradient) and d_row_weights
+ * (fp32 [rows], sum_j dh_j silu(g_j) u_j) are written unless NULL.
+ * Errors: INVALID_ARG, CUDA.
+ */
+moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int64_t lddh, int32_t rows, int32_t f,
+                               const float* row_weights, const int32_t* n_rows, void* dgu, int64_t lddgu, void* h,
+                               int64_t ldh, float* d_row_weights, uint32_t flags, void* stream);
+
+/*
+ * Synchronise the current device and return the first device-side error that
+ * one of these operators recorded on it since the last call (then clear it):
+ * MOE_ERR_TIMEOUT or MOE_OK; MOE_ERR_CUDA if the synchronisation failed.
+ */
+moe_status moe_check_op_status(void);
+
 /* Static text for a status code. */
 const char* moe_status_string(moe_status s);
 

@@ -215,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 const uint32_t bytes = kHalfTile + (WG || nbox == 0 ? kHalfTile : nbox * 32 * 128);
                 for (int s = 0; s < KS; ++s, ++j) {
                     const int st = j % kGroupedStages;
-                    if (j >= kGroupedStages) ok = tc::bar_wait_cluster(&empty_bar[st], ((j / kGroupedStages) - 1) & 1, g.status);
+                    if (j >= kGroupedStages) ok = tc::bar_wait(&empty_bar[st], ((j / kGroupedStages) - 1) & 1, g.status);
                     if (!ok) break;
                     uint8_t* As = smem + st * kGroupedStage;
                     uint8_t* Bs = As + kHalfTile;
@@ -269,7 +269,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         tc::fence_after();
                     }
                     const uint32_t acc_addr = tmem + (it & 1) * 256;
-                    ok = tc::bar_wait_cluster(&full_bar[st], (j / kGroupedStages) & 1, g.status);
+                    // (a cleared step is released by a thread of the other CTA, any other by copies alone)
+                    if (WG && s == KS - 1 && (tl.n & 15)) ok = tc::bar_wait_cluster(&full_bar[st], (j / kGroupedStages) & 1, g.status);
+                    else ok = tc::bar_wait(&full_bar[st], (j / kGroupedStages) & 1, g.status);
                     if (!ok) break;
                     tc::fence_after();
                     const uint32_t a_addr = smem_addr(smem + st * kGroupedStage), b_addr = a_addr + kHalfTile;
@@ -298,7 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             if (!(tl.n & 15)) continue;
             const int st = (j - 1) % kGroupedStages;
             ok = true;
-            if (lane == 0) ok = tc::bar_wait_cluster(&tail_bar[st], (phases >> st) & 1, g.status);
+            if (lane == 0) ok = tc::bar_wait(&tail_bar[st], (phases >> st) & 1, g.status);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
             phases ^= 1u << st;
@@ -330,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 const bool add = OUT32 && (part > 0 || g.accumulate);
                 if (!empty) {
                     ++it;
-                    if (lane == 0) ok = tc::bar_wait_cluster(&accf_bar[b], use & 1, g.status);
+                    if (lane == 0) ok = tc::bar_wait(&accf_bar[b], use & 1, g.status);
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     if (!ok) break;
                     tc::fence_after();

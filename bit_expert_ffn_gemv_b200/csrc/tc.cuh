@@ -127,8 +127,10 @@ MOE_DEV void cluster_sync() {
 MOE_DEV void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// (relaxed: announces a copy's bytes, publishes no memory of this thread; a
+// release here drains the thread's outstanding operations, ~0.7 us per step)
 MOE_DEV void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 // bar_wait for a barrier that other CTAs of the cluster arrive on

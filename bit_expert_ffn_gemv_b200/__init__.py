@@ -23,7 +23,7 @@ __all__ = ["MoeError", "MoeConfig", "MoeLayerWeights", "MoeLayer", "lib", "libra
            "moe_get_stats", "moe_status_string", "moe_profile", "moe_profile_read", "moe_kernel_name", "MoeStats",
            "moe_debug_router_logits", "moe_router_error_depth", "moe_rms_normalize", "rms_normalize",
            "moe_set_expert_range", "moe_debug_wait_limit", "MOE_OP_FP16", "MOE_OP_TRANSPOSE", "moe_check_op_status",
-           "grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward"]
+           "grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "adapter_project", "MoeAdapterArgs"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmoe.so")
@@ -65,6 +65,14 @@ MOE_KERNEL_COUNT = 13
 class MoeLayerWeights(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("router_w", ctypes.c_void_p),
                 ("router_bias", ctypes.c_void_p)]
+
+
+class MoeAdapterArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("tokens", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("w", ctypes.c_void_p), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("n_adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lock = threading.Lock()
@@ -130,6 +138,10 @@ def lib() -> ctypes.CDLL:
             L.moe_swiglu.argtypes = [vp, i64, i32, i32, vp, vp, vp, i64, u32, vp]
             L.moe_swiglu_backward.restype = st
             L.moe_swiglu_backward.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp, u32, vp]
+            L.moe_adapter_workspace.restype = ctypes.c_size_t
+            L.moe_adapter_workspace.argtypes = [i32, i32, i32]
+            L.moe_adapter_project.restype = st
+            L.moe_adapter_project.argtypes = [ctypes.POINTER(MoeAdapterArgs), u32, vp]
             L.moe_check_op_status.restype = st
             L.moe_check_op_status.argtypes = []
             L.moe_status_string.restype = ctypes.c_char_p
@@ -388,7 +400,7 @@ class MoeLayer:
 
 def __getattr__(name):
     # the 16-bit operators work on torch tensors: their module imports torch, so it loads on first use
-    if name in ("grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward"):
+    if name in ("grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "adapter_project"):
         from . import experts16
         fn = getattr(experts16, name)
         globals()[name] = fn

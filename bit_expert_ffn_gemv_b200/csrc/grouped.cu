@@ -32,6 +32,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "adapter.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -39,12 +40,15 @@
 namespace moe {
 
 constexpr int kGroupedThreads = 256;
-constexpr int kGroupedStages = 6;
 constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an operand, one K = 64 step
 constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
-constexpr int kGroupedSmem = kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + 1024;
+// with adapters the epilogue's warps also hold their tokens' v, in place of the sixth step
+constexpr int grouped_stages(bool adapt) { return adapt ? 5 : 6; }
+constexpr int grouped_smem(bool adapt) {
+    return grouped_stages(adapt) * kGroupedStage + 4 * kEpiWarpBytes + (adapt ? 4 * kAdapterV * 4 : 0) + 1024;
+}
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
 // 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
@@ -52,7 +56,7 @@ constexpr int kGroupedMaxGroups = 1024;
 // many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
 // by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
 constexpr int kPartSteps = 8;
-static_assert(kGroupedSmem + 8 * (kGroupedMaxGroups + 8) <= 227 * 1024, "shared memory");
+static_assert(grouped_smem(false) + 8 * (kGroupedMaxGroups + 8) <= 227 * 1024, "shared memory");
 
 struct GroupedMaps {
     CUtensorMap a, b, b_small;
@@ -118,11 +122,12 @@ MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int64_t t, const int* start, c
     return r;
 }
 
-template <int MODE, bool OUT32>
+template <int MODE, bool OUT32, bool ADAPT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
-    grouped_kernel(const GroupedArgs g, const __grid_constant__ CUtensorMap amap,
+    grouped_kernel(const GroupedArgs g, const AdapterArgs ad, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap bmap_s) {
     constexpr bool WG = MODE == kGroupedWeights;
+    constexpr int kGroupedStages = grouped_stages(ADAPT);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[kGroupedStages], empty_bar[kGroupedStages], tail_bar[kGroupedStages];
     __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
@@ -151,7 +156,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     // group starts, clamped into [0, M] and kept ascending (a bad table reads
     // and writes nothing out of range); pre = prefix sum of the groups' row
     // blocks, or (weights) each group's row count
-    for (int i = tid; i <= g.E; i += kGroupedThreads) start[i] = min(max(__ldg(&g.offsets[i]), 0), g.M);
+    for (int i = tid; i <= g.E; i += kGroupedThreads)
+        start[i] = ADAPT ? (i ? g.M : 0) : min(max(__ldg(&g.offsets[i]), 0), g.M);  // (adapters: one group)
     __syncthreads();
     constexpr int kPer = (kGroupedMaxGroups + kGroupedThreads - 1) / kGroupedThreads;
     int blocks[kPer], mine = 0;
@@ -321,6 +327,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true;
         int it = 0;
         const bool bf16 = g.bf16 != 0;
+        float* vbuf = reinterpret_cast<float*>(smem + kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes) + q * kAdapterV;
+        if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
         for (int64_t t = pair; t < total && ok; t += pairs) {
             const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
             const bool empty = WG && tl.n == 0;
@@ -346,21 +354,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     const bool in = f + seg * kVec < g.F;
                     const int64_t at = (int64_t)tl.row0 * g.ldo + f + seg * kVec;
                     uint32_t r[16];
+                    AdapterRow arow;
                     tc::ld16_nowait(tb, r);
                     tc::ld_wait();
                     for (int c0 = 0; c0 < tl.n; c0 += 16) {
+                        if (ADAPT) {
+                            float acc[16];
+                            const int m = min(16, tl.n - c0);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[i] = __uint_as_float(r[i]);
+                            if (part == 0) {
+                                if (bf16) adapter_delta<true>(ad, tl.row0 + c0, m, f + lane, vbuf, arow, acc);
+                                else adapter_delta<false>(ad, tl.row0 + c0, m, f + lane, vbuf, arow, acc);
+                            }
+                            if (!OUT32 && g.accumulate && f + lane < g.F) {
+                                const uint16_t* y = static_cast<const uint16_t*>(g.out) + (int64_t)(tl.row0 + c0) * g.ldo + f + lane;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (i < m) {
+                                        const uint16_t was = y[(int64_t)i * g.ldo];
+                                        acc[i] += bf16 ? unpack1<true>(was) : unpack1<false>(was);
+                                    }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(acc[i]);
+                        }
                         if (OUT32) {
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(stg)[i * 32 + lane] = r[i];
                         } else {
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 reinterpret_cast<uint16_t*>(stg)[i * 32 + lane] = to16(__uint_as_float(r[i]), bf16);
                         }
                         const bool more = c0 + 16 < tl.n;
                         if (more) tc::ld16_nowait(tb + c0 + 16, r);
                         __syncwarp();
-    #pragma unroll
+#pragma unroll
                         for (int p = 0; p < 16 / kRowsPer; ++p) {
                             const int row = p * kRowsPer + vr;
                             if (in && c0 + row < tl.n) {
@@ -378,24 +408,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     constexpr int kCols = OUT32 ? 32 : 64, kVec = OUT32 ? 4 : 8;
                     for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
                         if (empty) {
-    #pragma unroll
+#pragma unroll
                             for (int p = 0; p < 8; ++p)
                                 *reinterpret_cast<uint4*>(stg + lane * 128 + p * 16) = make_uint4(0, 0, 0, 0);
                         } else {
-    #pragma unroll
+#pragma unroll
                             for (int h = 0; h < kCols; h += 32) {
                                 uint32_t r[32];
                                 tc::ld16_nowait(tb + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
                                 tc::ld16_nowait(tb + c0 + h + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
                                 tc::ld_wait();
-    #pragma unroll
+#pragma unroll
                                 for (int p = 0; p < 32 / kVec; ++p) {
                                     uint4 v;
                                     if (OUT32) {
                                         v = make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
                                     } else {
                                         uint32_t w[4];
-    #pragma unroll
+#pragma unroll
                                         for (int i = 0; i < 4; ++i)
                                             w[i] = pack16(__uint_as_float(r[(8 * p + 2 * i) & 31]),
                                                           __uint_as_float(r[(8 * p + 2 * i + 1) & 31]), bf16);
@@ -408,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         }
                         __syncwarp();
                         const int col = tl.g0 + c0 + (lane & 7) * kVec;
-    #pragma unroll
+#pragma unroll
                         for (int p = 0; p < 8; ++p) {
                             const int row = p * 4 + (lane >> 3);
                             if (f + row < g.F && col < g.C) {
@@ -458,12 +488,62 @@ static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t r
 
 template <int MODE, bool OUT32>
 static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
-    auto kern = grouped_kernel<MODE, OUT32>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGroupedSmem);
+    auto kern = grouped_kernel<MODE, OUT32, false>;
+    constexpr int smem = grouped_smem(false);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
-    kern<<<2 * pairs, kGroupedThreads, kGroupedSmem, s>>>(g, m.a, m.b, m.b_small);
+    kern<<<2 * pairs, kGroupedThreads, smem, s>>>(g, AdapterArgs{}, m.a, m.b, m.b_small);
     return cudaGetLastError();
+}
+
+// maps of the forward and rows products: W as [E][N][K], whose rows (forward) or columns are the features
+static cudaError_t product_maps(GroupedMaps* m, bool forward, bool bf, int E, int N, int K, const void* w,
+                                const void* rows, int64_t M, int64_t ld) {
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
+    const cuuint64_t str[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
+    const cuuint32_t box[3] = {64, forward ? 128u : 64u, 1};
+    cudaError_t e = encode_sw128(&m->a, bf, w, 3, dims, str, box);
+    if (e == cudaSuccess) e = map_2d(&m->b, bf, rows, M, forward ? K : N, ld, 128);
+    if (e == cudaSuccess) e = map_2d(&m->b_small, bf, rows, M, forward ? K : N, ld, 32);
+    return e;
+}
+
+template <bool OUT32>
+static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t s) {
+    GroupedMaps m;
+    cudaError_t e = product_maps(&m, true, bf16, 1, p.N, p.K, p.w, p.x, p.T, p.ldx);
+    if (e != cudaSuccess) return e;
+    GroupedArgs g{};
+    g.E = 1;
+    g.M = p.T;
+    g.F = p.N;
+    g.C = p.K;
+    g.out = p.y;
+    g.ldo = p.ldy;
+    g.bf16 = bf16 ? 1 : 0;
+    g.accumulate = p.accumulate;
+    g.status = p.status;
+    auto kern = grouped_kernel<kGroupedForward, OUT32, true>;
+    constexpr int smem = grouped_smem(true);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * (unsigned)(tiles < sm_count() / 2 ? tiles : sm_count() / 2));
+    cfg.blockDim = kGroupedThreads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, g, p, m.a, m.b, m.b_small);
+}
+
+cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {
+    return out32 ? adapter_launch<true>(p, bf16, s) : adapter_launch<false>(p, bf16, s);
 }
 
 cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const void* x, int64_t ldx, const void* dy,
@@ -481,16 +561,10 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const 
         return out_fp32 ? grouped_launch<kGroupedWeights, true>(g, m, tiles, s)
                         : grouped_launch<kGroupedWeights, false>(g, m, tiles, s);
     }
-    // W as [E][N][K]: the features are its rows (forward) or its columns (rows gradient)
-    const int N = mode == kGroupedForward ? g.F : g.C, K = mode == kGroupedForward ? g.C : g.F;
-    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)g.E};
-    const cuuint64_t str[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
-    const cuuint32_t box[3] = {64, mode == kGroupedForward ? 128u : 64u, 1};
-    e = encode_sw128(&m.a, bf, w, 3, dims, str, box);
-    const void* rows = mode == kGroupedForward ? x : dy;
-    const int64_t ld = mode == kGroupedForward ? ldx : lddy;
-    if (e == cudaSuccess) e = map_2d(&m.b, bf, rows, g.M, g.C, ld, 128);
-    if (e == cudaSuccess) e = map_2d(&m.b_small, bf, rows, g.M, g.C, ld, 32);
+    const bool forward = mode == kGroupedForward;
+    if (forward && g.M <= kSkinnyMaxRows) return launch_skinny_grouped(g, w, x, ldx, out_fp32, s);
+    e = product_maps(&m, forward, bf, g.E, forward ? g.F : g.C, forward ? g.C : g.F, w, forward ? x : dy, g.M,
+                     forward ? ldx : lddy);
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((int64_t)(g.M + 255) / 256 + (g.E < g.M ? g.E : g.M)) * JT;
     if (mode == kGroupedForward)

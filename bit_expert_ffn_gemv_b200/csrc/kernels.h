@@ -198,4 +198,31 @@ struct SwigluArgs {
 };
 cudaError_t launch_swiglu(const SwigluArgs& a, bool bf16, bool grad, cudaStream_t s);
 
+// Products of at most this many rows take the warp-MMA kernel (skinny.cu).
+constexpr int kSkinnyMaxRows = 64;
+cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const void* x, int64_t ldx, bool out32,
+                                  cudaStream_t s);
+
+// Low-rank adapters beside a projection.
+struct AdapterArgs {
+    const void* x;       // [T x K], pitch ldx
+    int64_t ldx;
+    int T, N, K, L, r;
+    const void* w;       // [N x K] or null
+    const void* a;       // [L x r x K]
+    const void* b;       // [L x N x r]
+    const float* scale;  // [L] or null
+    const int32_t* ids;  // [T]
+    void* y;             // [T x N], pitch ldy
+    int64_t ldy;
+    float* v;            // workspace [slices x T x r]: scale * A x, per slice of K
+    int slices;
+    int accumulate;
+    uint32_t* status;
+};
+int adapter_slices(int T, int K);
+cudaError_t launch_adapters(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s);
+cudaError_t launch_skinny_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s);
+cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,207 @@
+// skinny.cu -- products of few rows with 16-bit matrices: every matrix value is
+// read once from HBM, straight into the registers of a warp-level MMA.
+//
+// One CTA: 16 features of one matrix by the (at most 64) rows that use it; its
+// eight warps split K.  Features are the MMA's M, rows its N in blocks of 8;
+// both operands load 16 bytes a lane in the same permuted order of k, so no
+// shared memory sits between HBM and the tensor core and no padded row tile is
+// computed.  The warps' sums meet in shared memory in warp order
+// (deterministic).  Bound by HBM: 2 N K bytes per matrix.
+//
+// Grouped form: a row's CTA looks its group up in the offsets (one round of
+// loads) and works only if it is the group's first row, so no list of groups
+// is built beforehand.  Adapter form: one matrix, then the tokens' deltas.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "pack16.cuh"
+
+namespace moe {
+
+constexpr int kSkinnyThreads = 256;
+
+struct SkinnyArgs {
+    const void* w;       // [groups x F x K]
+    const void* x;       // rows, pitch ldx
+    int64_t ldx;
+    int F, K;
+    const int32_t* offsets;  // grouped form
+    int E, M;
+    void* y;
+    int64_t ldy;
+    AdapterArgs ad;      // adapter form
+};
+
+template <bool BF16, int NB>
+MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t* x, int64_t ldx, int n, int kb, int ke,
+                         float* red, int pitch) {
+    const int lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
+    float acc[NB][4] = {};
+    const uint16_t* xr[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) xr[b] = x + (int64_t)min(b * 8 + gq, n - 1) * ldx;
+    constexpr int U = 4;  // 32-wide steps in flight
+    for (int k0 = kb; k0 < ke; k0 += 32 * U) {
+        uint4 lo[U], hi[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + 32 * u + 8 * c;
+            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+            if (k < ke) {
+                lo[u] = __ldcs(reinterpret_cast<const uint4*>(w0 + k));
+                hi[u] = __ldcs(reinterpret_cast<const uint4*>(w1 + k));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + 32 * u + 8 * c;
+            uint4 bv[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                bv[b] = make_uint4(0, 0, 0, 0);
+                if (k < ke) bv[b] = __ldg(reinterpret_cast<const uint4*>(xr[b] + k));
+            }
+            const uint32_t f0[4] = {lo[u].x, hi[u].x, lo[u].y, hi[u].y}, f1[4] = {lo[u].z, hi[u].z, lo[u].w, hi[u].w};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                mma16<BF16>(acc[b], f0, bv[b].x, bv[b].y);
+                mma16<BF16>(acc[b], f1, bv[b].z, bv[b].w);
+            }
+        }
+    }
+    // [feature][row]
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        red[gq * pitch + b * 8 + 2 * c] = acc[b][0];
+        red[gq * pitch + b * 8 + 2 * c + 1] = acc[b][1];
+        red[(gq + 8) * pitch + b * 8 + 2 * c] = acc[b][2];
+        red[(gq + 8) * pitch + b * 8 + 2 * c + 1] = acc[b][3];
+    }
+}
+
+template <bool BF16, bool OUT32, bool ADAPT>
+__global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyArgs p) {
+    constexpr int kPitch = kSkinnyMaxRows + 1;
+    __shared__ float red[8][16 * kPitch];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
+    int e = 0, row0 = 0, n = ADAPT ? p.ad.T : 0;
+    if (!ADAPT) {
+        const int r = blockIdx.y;
+        if (tid == 0) found[1] = -1;
+        __syncthreads();
+        for (int i = tid; i < p.E; i += kSkinnyThreads) {
+            const int a = min(max(__ldg(&p.offsets[i]), 0), p.M), b = min(max(__ldg(&p.offsets[i + 1]), 0), p.M);
+            if (a == r && b > r) {  // (a table that is not ascending may name a row twice: one group wins)
+                found[0] = i;
+                found[1] = a;
+                found[2] = b - a;
+            }
+        }
+        __syncthreads();
+        if (found[1] < 0) return;
+        e = found[0];
+        row0 = found[1];
+        n = found[2];
+    }
+    const int f0 = blockIdx.x * 16;
+    const uint16_t* w = static_cast<const uint16_t*>(p.w) + ((int64_t)e * p.F + f0) * p.K;
+    const uint16_t* w0 = w + (int64_t)gq * p.K;
+    const uint16_t* w1 = w + (int64_t)(f0 + gq + 8 < p.F ? gq + 8 : gq) * p.K;
+    const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)row0 * p.ldx;
+    const int kw = (((p.K + 7) >> 3) + 31) & ~31, kb = warp * kw, ke = min(p.K, kb + kw);
+    if (n <= 8) skinny_sums<BF16, 1>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (n <= 16) skinny_sums<BF16, 2>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    __syncthreads();
+    if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = tid; i < 16 * n; i += kSkinnyThreads) {
+        const int m = i >> 4, j = i & 15, f = f0 + j;
+        if (f >= p.F) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += red[q][j * kPitch + m];
+        const int64_t o = (int64_t)(row0 + m) * p.ldy + f;
+        if (ADAPT) {
+            const AdapterArgs& ad = p.ad;
+            const int a = __ldg(&ad.ids[m]);
+            if (a >= 0 && a < ad.L) {
+                const uint16_t* br = static_cast<const uint16_t*>(ad.b) + ((int64_t)a * ad.N + f) * ad.r;
+                const float* v = ad.v + (int64_t)m * ad.r;
+                float dlt = 0.f;
+                for (int q = 0; q < ad.r; q += 8) {
+                    float b[8];
+                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(br + q)), b);
+                    float vv[8] = {};
+                    for (int sl = 0; sl < ad.slices; ++sl) {
+                        const float4* q4 = reinterpret_cast<const float4*>(v + (int64_t)sl * ad.T * ad.r + q);
+                        const float4 u0 = q4[0], u1 = q4[1];
+                        vv[0] += u0.x, vv[1] += u0.y, vv[2] += u0.z, vv[3] += u0.w;
+                        vv[4] += u1.x, vv[5] += u1.y, vv[6] += u1.z, vv[7] += u1.w;
+                    }
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) dlt = fmaf(b[z], vv[z], dlt);
+                }
+                s += dlt;
+            }
+            if (ad.accumulate)
+                s += OUT32 ? static_cast<const float*>(p.y)[o] : unpack1<BF16>(static_cast<const uint16_t*>(p.y)[o]);
+        }
+        if (OUT32) static_cast<float*>(p.y)[o] = s;
+        else static_cast<uint16_t*>(p.y)[o] = pack1<BF16>(s);
+    }
+}
+
+cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const void* x, int64_t ldx, bool out32,
+                                  cudaStream_t s) {
+    SkinnyArgs p{};
+    p.w = w;
+    p.x = x;
+    p.ldx = ldx;
+    p.F = g.F;
+    p.K = g.C;
+    p.offsets = g.offsets;
+    p.E = g.E;
+    p.M = g.M;
+    p.y = g.out;
+    p.ldy = g.ldo;
+    const dim3 grid((g.F + 15) / 16, g.M);
+    if (g.bf16) {
+        if (out32) skinny_kernel<true, true, false><<<grid, kSkinnyThreads, 0, s>>>(p);
+        else skinny_kernel<true, false, false><<<grid, kSkinnyThreads, 0, s>>>(p);
+    } else {
+        if (out32) skinny_kernel<false, true, false><<<grid, kSkinnyThreads, 0, s>>>(p);
+        else skinny_kernel<false, false, false><<<grid, kSkinnyThreads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_skinny_adapter(const AdapterArgs& a, bool bf16, bool out32, cudaStream_t s) {
+    SkinnyArgs p{};
+    p.w = a.w;
+    p.x = a.x;
+    p.ldx = a.ldx;
+    p.F = a.N;
+    p.K = a.K;
+    p.y = a.y;
+    p.ldy = a.ldy;
+    p.ad = a;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((a.N + 15) / 16);
+    cfg.blockDim = kSkinnyThreads;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (bf16)
+        return out32 ? cudaLaunchKernelEx(&cfg, skinny_kernel<true, true, true>, p)
+                     : cudaLaunchKernelEx(&cfg, skinny_kernel<true, false, true>, p);
+    return out32 ? cudaLaunchKernelEx(&cfg, skinny_kernel<false, true, true>, p)
+                 : cudaLaunchKernelEx(&cfg, skinny_kernel<false, false, true>, p);
+}
+
+}  // namespace moe

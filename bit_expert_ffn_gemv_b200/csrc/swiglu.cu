@@ -14,39 +14,10 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pack16.cuh"
 
 namespace moe {
 
-template <bool BF16>
-MOE_DEV void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (BF16) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        } else {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            f[2 * i] = p.x;
-            f[2 * i + 1] = p.y;
-        }
-    }
-}
-template <bool BF16>
-MOE_DEV uint4 pack8(const float (&f)[8]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (BF16) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&p);
-        } else {
-            const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
-}
 MOE_DEV float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 constexpr int kSwigluThreads = 256;

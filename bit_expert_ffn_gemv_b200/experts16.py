@@ -22,11 +22,13 @@ Rows outside every group are left as they were in a given ``out``, and are unset
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
-from . import MOE_ACCUMULATE, MOE_OP_FP16, MOE_OP_TRANSPOSE, MOE_OUT_FP32, _check, lib
+from . import MOE_ACCUMULATE, MOE_OP_FP16, MOE_OP_TRANSPOSE, MOE_OUT_FP32, MoeAdapterArgs, _check, lib
 
-__all__ = ["grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward"]
+__all__ = ["grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "adapter_project"]
 
 _TYPES = (torch.bfloat16, torch.float16)
 
@@ -170,3 +172,36 @@ def swiglu_backward(gu, dh, row_weights=None, dgu=None, h=None, drw=None, with_h
              dh.data_ptr(), _pitch(dh), rows, f, _ptr(row_weights), _ptr(n_rows), dgu.data_ptr(), _pitch(dgu), _ptr(h),
              _pitch(h) if h is not None else 0, _ptr(drw), _type_flag(gu))
     return dgu, h, drw
+
+
+def adapter_project(x, a, b, ids, w=None, scale=None, out=None, flags=0, stream=None):
+    """[w x_t +] scale[i] * b[i] (a[i] x_t) for every token t with its adapter i = ids[t]: x [T, k], a [L, rank, k],
+    b [L, n, rank], ids int32 [T], w [n, k], scale fp32 [L] -> [T, n], x's type, or fp32 with MOE_OUT_FP32 in flags.
+    With MOE_ACCUMULATE the result is added to out.  An id outside [0, L): no adapter."""
+    _operand(x, "x")
+    for t, name in ((a, "a"), (b, "b")):
+        _need(t.dim() == 3 and t.is_cuda and t.device == x.device and t.dtype == x.dtype and t.is_contiguous(),
+              f"{name}: a contiguous 3-D tensor of x's type and device")
+    T, k = x.shape
+    L, rank, n = a.shape[0], a.shape[1], b.shape[1]
+    _need(a.shape[2] == k and tuple(b.shape) == (L, n, rank), f"a {tuple(a.shape)}, b {tuple(b.shape)} and x do not match")
+    _vector(ids, "ids", x, torch.int32, T)
+    if w is not None:
+        _need(tuple(w.shape) == (n, k) and w.device == x.device and w.dtype == x.dtype and w.is_contiguous(),
+              f"w: a contiguous {(n, k)} tensor of x's type and device")
+    if scale is not None:
+        _vector(scale, "scale", x, torch.float32, L)
+    dt = torch.float32 if flags & MOE_OUT_FP32 else x.dtype
+    _need(out is not None or not flags & MOE_ACCUMULATE, "MOE_ACCUMULATE adds to a given out")
+    if out is None:
+        out = torch.empty((T, n), dtype=dt, device=x.device)
+    _matrix(out, "out", x, n, T, (dt,))
+    size = lib().moe_adapter_workspace(T, k, rank)
+    ws = torch.empty(size, dtype=torch.uint8, device=x.device)
+    if stream is not None:
+        ws.record_stream(stream)  # freed below, possibly before the call has run on its stream
+    args = MoeAdapterArgs(x.data_ptr(), _pitch(x), T, n, k, _ptr(w), a.data_ptr(), b.data_ptr(), _ptr(scale),
+                          ids.data_ptr(), L, rank, out.data_ptr(), _pitch(out), ws.data_ptr(), size)
+    _enqueue(x.device, stream, "moe_adapter_project", lib().moe_adapter_project, ctypes.byref(args),
+             flags | _type_flag(x))
+    return out

@@ -56,6 +56,7 @@
 #ifndef MOE_H
 #define MOE_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -460,6 +461,45 @@ moe_status moe_swiglu(const void* gu, int64_t ldgu, int32_t rows, int32_t f, con
 moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int64_t lddh, int32_t rows, int32_t f,
                                const float* row_weights, const int32_t* n_rows, void* dgu, int64_t lddgu, void* h,
                                int64_t ldh, float* d_row_weights, uint32_t flags, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (the pages have
+ * no counterpart; it is the serving form of tuned variants of one model):
+ *   y[t] = [y[t] +] [W x[t] +] scale[a] * B_a (A_a x[t]),  a = ids[t]
+ * W and its product are left out when w is NULL; y[t] is added to with
+ * MOE_ACCUMULATE.  A token whose id lies outside [0, n_adapters) has no adapter
+ * term (without w and MOE_ACCUMULATE its row is zeros).  Tokens may come in any
+ * order of ids; runs of one adapter are fastest.  Adapters of a smaller rank
+ * are padded with zeros.  The inner product A x and the sum stay in fp32; y is
+ * rounded once.
+ */
+typedef struct {
+    const void* x;      /* [tokens x k], pitch ldx */
+    int64_t ldx;
+    int32_t tokens;     /* >= 0 */
+    int32_t n, k;       /* multiples of 8 */
+    const void* w;      /* [n x k] contiguous, or NULL */
+    const void* a;      /* [n_adapters x rank x k] contiguous */
+    const void* b;      /* [n_adapters x n x rank] contiguous */
+    const float* scale; /* [n_adapters], or NULL (1) */
+    const int32_t* ids; /* [tokens] */
+    int32_t n_adapters; /* >= 1 */
+    int32_t rank;       /* multiple of 8, 8..256 */
+    void* y;            /* [tokens x n], pitch ldy; 16-bit, or fp32 with MOE_OUT_FP32 */
+    int64_t ldy;
+    void* workspace;    /* moe_adapter_workspace bytes, 16-byte aligned, this call's own until it has run */
+    size_t workspace_bytes;
+} moe_adapter_args;
+
+/* Workspace bytes of moe_adapter_project (0 for arguments out of range). */
+size_t moe_adapter_workspace(int32_t tokens, int32_t k, int32_t rank);
+
+/*
+ * x and y must not overlap.  Errors: INVALID_ARG (a field out of the ranges
+ * above, a short pitch or workspace, NULL or misaligned pointer, y == x,
+ * unknown flag), CUDA.
+ */
+moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, void* stream);
 
 /*
  * Synchronise the current device and return the first device-side error that

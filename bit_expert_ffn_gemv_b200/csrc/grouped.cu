@@ -44,10 +44,10 @@ constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an
 constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
-// with adapters the epilogue's warps also hold their tokens' v, in place of the sixth step
+// with adapters the epilogue's warps also hold an fp32 block each, in place of the sixth step
 constexpr int grouped_stages(bool adapt) { return adapt ? 5 : 6; }
 constexpr int grouped_smem(bool adapt) {
-    return grouped_stages(adapt) * kGroupedStage + 4 * kEpiWarpBytes + (adapt ? 4 * kAdapterV * 4 : 0) + 1024;
+    return grouped_stages(adapt) * kGroupedStage + 4 * kEpiWarpBytes + (adapt ? 4 * kBlockBytes : 0) + 1024;
 }
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true;
         int it = 0;
         const bool bf16 = g.bf16 != 0;
-        float* vbuf = reinterpret_cast<float*>(smem + kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes) + q * kAdapterV;
+        float* block = reinterpret_cast<float*>(smem + kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + q * kBlockBytes);
         if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
         for (int64_t t = pair; t < total && ok; t += pairs) {
             const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
@@ -354,30 +354,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     const bool in = f + seg * kVec < g.F;
                     const int64_t at = (int64_t)tl.row0 * g.ldo + f + seg * kVec;
                     uint32_t r[16];
-                    AdapterRow arow;
                     tc::ld16_nowait(tb, r);
                     tc::ld_wait();
                     for (int c0 = 0; c0 < tl.n; c0 += 16) {
-                        if (ADAPT) {
-                            float acc[16];
+                        if (ADAPT && part == 0) {  // the delta, through the fp32 block and back
                             const int m = min(16, tl.n - c0);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[i] = __uint_as_float(r[i]);
-                            if (part == 0) {
-                                if (bf16) adapter_delta<true>(ad, tl.row0 + c0, m, f + lane, vbuf, arow, acc);
-                                else adapter_delta<false>(ad, tl.row0 + c0, m, f + lane, vbuf, arow, acc);
-                            }
+                            for (int i = 0; i < 16; ++i) block[i * kBlockPitch + lane] = __uint_as_float(r[i]);
+                            __syncwarp();
+                            if (bf16) add_delta<true, OUT32 ? 3 : 2>(ad, tl.row0 + c0, m, f, block);
+                            else add_delta<false, 2>(ad, tl.row0 + c0, m, f, block);
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(block[i * kBlockPitch + lane]);
                             if (!OUT32 && g.accumulate && f + lane < g.F) {
                                 const uint16_t* y = static_cast<const uint16_t*>(g.out) + (int64_t)(tl.row0 + c0) * g.ldo + f + lane;
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
                                     if (i < m) {
                                         const uint16_t was = y[(int64_t)i * g.ldo];
-                                        acc[i] += bf16 ? unpack1<true>(was) : unpack1<false>(was);
+                                        r[i] = __float_as_uint(__uint_as_float(r[i]) + (bf16 ? unpack1<true>(was) : unpack1<false>(was)));
                                     }
                             }
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(acc[i]);
                         }
                         if (OUT32) {
 #pragma unroll

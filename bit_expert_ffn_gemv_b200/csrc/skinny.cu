@@ -83,7 +83,7 @@ MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t*
 template <bool BF16, bool OUT32, bool ADAPT>
 __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyArgs p) {
     constexpr int kPitch = kSkinnyMaxRows + 1;
-    __shared__ float red[8][16 * kPitch];
+    __shared__ __align__(16) float red[8][16 * kPitch];
     __shared__ int found[3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
     int e = 0, row0 = 0, n = ADAPT ? p.ad.T : 0;
@@ -116,41 +116,78 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
     else if (n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     else skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     __syncthreads();
-    if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < 16 * n; i += kSkinnyThreads) {
-        const int m = i >> 4, j = i & 15, f = f0 + j;
-        if (f >= p.F) continue;
-        float s = 0.f;
+    // thread: feature tid % 16, rows tid / 16 + 16 i
+    constexpr int kOut = 16 * kSkinnyMaxRows / kSkinnyThreads;
+    const int j = tid & 15, f = f0 + j, m0 = tid >> 4;
+    float s[kOut];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s += red[q][j * kPitch + m];
-        const int64_t o = (int64_t)(row0 + m) * p.ldy + f;
-        if (ADAPT) {
-            const AdapterArgs& ad = p.ad;
-            const int a = __ldg(&ad.ids[m]);
-            if (a >= 0 && a < ad.L) {
-                const uint16_t* br = static_cast<const uint16_t*>(ad.b) + ((int64_t)a * ad.N + f) * ad.r;
-                const float* v = ad.v + (int64_t)m * ad.r;
-                float dlt = 0.f;
-                for (int q = 0; q < ad.r; q += 8) {
-                    float b[8];
-                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(br + q)), b);
-                    float vv[8] = {};
-                    for (int sl = 0; sl < ad.slices; ++sl) {
-                        const float4* q4 = reinterpret_cast<const float4*>(v + (int64_t)sl * ad.T * ad.r + q);
-                        const float4 u0 = q4[0], u1 = q4[1];
-                        vv[0] += u0.x, vv[1] += u0.y, vv[2] += u0.z, vv[3] += u0.w;
-                        vv[4] += u1.x, vv[5] += u1.y, vv[6] += u1.z, vv[7] += u1.w;
-                    }
+    for (int i = 0; i < kOut; ++i) {
+        s[i] = 0.f;
+        if (m0 + 16 * i < n) {
 #pragma unroll
-                    for (int z = 0; z < 8; ++z) dlt = fmaf(b[z], vv[z], dlt);
-                }
-                s += dlt;
-            }
-            if (ad.accumulate)
-                s += OUT32 ? static_cast<const float*>(p.y)[o] : unpack1<BF16>(static_cast<const uint16_t*>(p.y)[o]);
+            for (int q = 0; q < 8; ++q) s[i] += red[q][j * kPitch + m0 + 16 * i];
         }
-        if (OUT32) static_cast<float*>(p.y)[o] = s;
-        else static_cast<uint16_t*>(p.y)[o] = pack1<BF16>(s);
+    }
+    if (ADAPT) {
+        const AdapterArgs& ad = p.ad;
+        int id[kOut];
+        const uint16_t* br[kOut];
+        uint4 ahead[kOut][2];  // the first 16 of each token's row of B, read before v is there
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+            const int m = m0 + 16 * i;
+            id[i] = m < n && f < p.F ? __ldg(&ad.ids[m]) : -1;
+            if (id[i] >= ad.L) id[i] = -1;
+            br[i] = static_cast<const uint16_t*>(ad.b) + ((int64_t)max(id[i], 0) * ad.N + min(f, p.F - 1)) * ad.r;
+            ahead[i][0] = ahead[i][1] = make_uint4(0, 0, 0, 0);
+            if (id[i] >= 0) {
+                ahead[i][0] = __ldg(reinterpret_cast<const uint4*>(br[i]));
+                if (ad.r > 8) ahead[i][1] = __ldg(reinterpret_cast<const uint4*>(br[i] + 8));
+            }
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        constexpr int kBlock = 64;  // rank values per pass
+        float* v = &red[0][0];      // [row][kBlock]: the sums above are in registers
+        static_assert(kSkinnyMaxRows * kBlock <= 8 * 16 * kPitch, "v fits over the sums");
+        for (int j0 = 0; j0 < ad.r; j0 += kBlock) {
+            const int nj = min(kBlock, ad.r - j0), quads = nj >> 2;
+            __syncthreads();
+            for (int i = tid; i < n * quads; i += kSkinnyThreads) {
+                const int m = i / quads, jq = (i - m * quads) * 4;
+                const float* src = ad.v + (int64_t)m * ad.r + j0 + jq;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int sl = 0; sl < ad.slices; ++sl) {
+                    const float4 u = *reinterpret_cast<const float4*>(src + (int64_t)sl * ad.T * ad.r);
+                    a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+                }
+                *reinterpret_cast<float4*>(v + m * kBlock + jq) = a;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+                if (id[i] < 0) continue;
+                const float* vm = v + (m0 + 16 * i) * kBlock;
+                for (int q = 0; q < nj; q += 8) {
+                    float b[8];
+                    unpack8<BF16>(j0 + q == 0 ? ahead[i][0] : j0 + q == 8 ? ahead[i][1]
+                                  : __ldg(reinterpret_cast<const uint4*>(br[i] + j0 + q)), b);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) s[i] = fmaf(b[z], vm[q + z], s[i]);
+                }
+            }
+        }
+    }
+    if (f >= p.F) return;
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+        const int m = m0 + 16 * i;
+        if (m >= n) continue;
+        const int64_t o = (int64_t)(row0 + m) * p.ldy + f;
+        if (ADAPT && p.ad.accumulate)
+            s[i] += OUT32 ? static_cast<const float*>(p.y)[o] : unpack1<BF16>(static_cast<const uint16_t*>(p.y)[o]);
+        if (OUT32) static_cast<float*>(p.y)[o] = s[i];
+        else static_cast<uint16_t*>(p.y)[o] = pack1<BF16>(s[i]);
     }
 }
 

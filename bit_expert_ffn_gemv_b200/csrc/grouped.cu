@@ -94,20 +94,20 @@ struct GroupedTile {
 // by a prefix sum over the groups, features innermost, so the CTAs that run
 // together share the group's rows and its matrix through L2.
 template <int MODE>
-MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int64_t t, const int* start, const int* pre, int JT) {
+MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const int* start, const int* pre, int JT) {
     GroupedTile r;
     if (MODE == kGroupedWeights) {
         const int per = JT * ((g.C + 255) >> 8);
-        r.e = (int)(t / per);
-        const int in = (int)(t - (int64_t)r.e * per);
+        r.e = t / per;
+        const int in = t - r.e * per;
         r.f0 = (in % JT) << 8;
         r.g0 = (in / JT) << 8;
         r.row0 = start[r.e];
         r.n = pre[r.e];
         return r;
     }
-    const int q = (int)(t / JT);
-    r.f0 = (int)(t - (int64_t)q * JT) << 8;
+    const int q = t / JT;
+    r.f0 = (t - q * JT) << 8;
     r.g0 = 0;
     int lo = 0, hi = g.E - 1;  // last group with pre <= q
     while (lo < hi) {
@@ -120,6 +120,28 @@ MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int64_t t, const int* start, c
     r.row0 = first;
     r.n = min(256, start[lo + 1] - first);
     return r;
+}
+
+// Exclusive scan (sum, or running maximum from `start`) of one value per thread
+// over the CTA; every thread calls it.
+template <bool MAX>
+MOE_DEV int block_exclusive(int v, int start, int* wsum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc = MAX ? max(inc, u) : inc + u;
+    }
+    int ex = __shfl_up_sync(0xffffffffu, inc, 1);
+    if (lane == 0) ex = start;
+    __syncthreads();  // (an earlier scan's sums have been read)
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kGroupedThreads / 32; ++w)
+        if (w < warp) ex = MAX ? max(ex, wsum[w]) : ex + wsum[w];
+    return ex;
 }
 
 template <int MODE, bool OUT32, bool ADAPT>
@@ -153,47 +175,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     }
     if (warp == 2) tc::tmem_alloc_pair(&tmem_slot, 512);
 
-    // group starts, clamped into [0, M] and kept ascending (a bad table reads
-    // and writes nothing out of range); pre = prefix sum of the groups' row
-    // blocks, or (weights) each group's row count
-    for (int i = tid; i <= g.E; i += kGroupedThreads)
-        start[i] = ADAPT ? (i ? g.M : 0) : min(max(__ldg(&g.offsets[i]), 0), g.M);  // (adapters: one group)
-    __syncthreads();
-    constexpr int kPer = (kGroupedMaxGroups + kGroupedThreads - 1) / kGroupedThreads;
-    int blocks[kPer], mine = 0;
+    // Group starts: clamped into [0, rows] and made ascending by a running
+    // maximum, so that a bad table reads and writes nothing out of range; pre =
+    // prefix sum of the groups' 256-row blocks, or (weights) each group's rows.
+    constexpr int kPer = kGroupedMaxGroups / kGroupedThreads;
+    const int first = ADAPT ? 0 : min(max(__ldg(&g.offsets[0]), 0), g.M);
+    int end[kPer], top = first;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
-        const int c = e < g.E ? max(start[e + 1] - start[e], 0) : 0;
-        if (WG && e < g.E) pre[e] = c;
-        blocks[i] = (c + 255) >> 8;
-        mine += blocks[i];
+        if (e < g.E) top = max(top, ADAPT ? g.M : min(max(__ldg(&g.offsets[e + 1]), 0), g.M));
+        end[i] = top;
     }
-    int64_t total;
+    const int top_before = block_exclusive<true>(top, first, wsum);
+    int begin = max(top_before, first), mine = 0, blocks[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i, stop = max(end[i], begin);
+        if (e < g.E) start[e] = begin;
+        if (e == g.E - 1) start[g.E] = stop;
+        if (WG && e < g.E) pre[e] = stop - begin;
+        blocks[i] = e < g.E ? (stop - begin + 255) >> 8 : 0;
+        mine += blocks[i];
+        begin = stop;
+    }
+    int total;
     if (WG) {
-        total = (int64_t)g.E * JT * ((g.C + 255) >> 8);
+        total = g.E * JT * ((g.C + 255) >> 8);
     } else {
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
-        int before = inc - mine, all = 0;
-#pragma unroll
-        for (int w = 0; w < kGroupedThreads / 32; ++w) {
-            if (w < warp) before += wsum[w];
-            all += wsum[w];
-        }
+        int before = block_exclusive<false>(mine, 0, wsum);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = tid * kPer + i;
             if (e < g.E) pre[e] = before;
             before += blocks[i];
+            if (e == g.E - 1) pre[g.E] = before;
         }
-        total = (int64_t)all * JT;
+        __syncthreads();
+        total = pre[g.E] * JT;
     }
     tc::fence_before();
     __syncthreads();
@@ -204,43 +223,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     const int KC = (g.C + 63) >> 6;  // steps per tile (forward, rows)
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ======================= loader
-            bool ok = true;
-            int j = 0;
-            uint32_t full_leader[kGroupedStages];
-#pragma unroll
-            for (int i = 0; i < kGroupedStages; ++i) full_leader[i] = tc::cluster_addr(&full_bar[i], 0);
-            for (int64_t t = pair; t < total && ok; t += pairs) {
-                const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
-                const int KS = WG ? (tl.n + 63) >> 6 : KC;
-                const int nh = WG ? 128 : ((tl.n + 31) & ~31) >> 1;
-                const int brow = tl.row0 + (int)rank * nh;
-                const int f = tl.f0 + (int)rank * 128;
-                const int nbox = nh > 64 ? 0 : (nh + 31) >> 5;  // 32-row boxes (0: one of 128 rows)
-                const uint32_t bytes = kHalfTile + (WG || nbox == 0 ? kHalfTile : nbox * 32 * 128);
-                for (int s = 0; s < KS; ++s, ++j) {
-                    const int st = j % kGroupedStages;
-                    if (j >= kGroupedStages) ok = tc::bar_wait(&empty_bar[st], ((j / kGroupedStages) - 1) & 1, g.status);
-                    if (!ok) break;
-                    uint8_t* As = smem + st * kGroupedStage;
-                    uint8_t* Bs = As + kHalfTile;
-                    // a last step that ends inside 16 rows is completed by warp 2 once it is cleared
-                    const bool tail = WG && s == KS - 1 && (tl.n & 15);
-                    uint32_t bar;
-                    if (tail) {
-                        mbar_arrive_expect_tx(&tail_bar[st], bytes);
-                        bar = tc::cluster_addr(&tail_bar[st], rank);
-                    } else {
-                        bar = full_leader[0] + (uint32_t)st * 8u;
-                        tc::arrive_expect_cluster(bar, bytes);
-                    }
+        // ======================= loader (the whole warp walks, one lane issues)
+        const bool one = tc::elect_one();
+        const uint32_t full_leader = tc::cluster_addr(&full_bar[0], 0), tail_own = tc::cluster_addr(&tail_bar[0], rank);
+        bool ok = true, filled = false;  // filled: every stage has been used once
+        int st = 0;
+        uint32_t phase = 1;  // parity of the stage's last "empty" (0 once every stage has been used)
+        for (int t = pair; t < total && ok; t += pairs) {
+            const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+            const int KS = WG ? (tl.n + 63) >> 6 : KC;
+            const int nh = WG ? 128 : ((tl.n + 31) & ~31) >> 1;
+            const int brow = tl.row0 + (int)rank * nh;
+            const int f = tl.f0 + (int)rank * 128, gc = tl.g0 + (int)rank * 128;
+            const int nbox = nh > 64 ? 0 : (nh + 31) >> 5;  // 32-row boxes (0: one of 128 rows)
+            const uint32_t bytes = kHalfTile + (WG || nbox == 0 ? kHalfTile : nbox * 32 * 128);
+            for (int s = 0; s < KS; ++s) {
+                if (filled) ok = tc::bar_wait(&empty_bar[st], phase, g.status);
+                if (!ok) break;
+                uint8_t* As = smem + st * kGroupedStage;
+                uint8_t* Bs = As + kHalfTile;
+                // a last step that ends inside 16 rows is completed by warp 2 once it is cleared
+                const bool tail = WG && s == KS - 1 && (tl.n & 15);
+                const uint32_t bar = (tail ? tail_own : full_leader) + (uint32_t)st * 8u;
+                if (one) {
+                    if (tail) mbar_arrive_expect_tx(&tail_bar[st], bytes);
+                    else tc::arrive_expect_cluster(bar, bytes);
                     if (WG) {
                         const int r = tl.row0 + s * 64;
                         tc::tma_2d_pair(As, &amap, f, r, bar);
                         tc::tma_2d_pair(As + kPanel, &amap, f + 64, r, bar);
-                        tc::tma_2d_pair(Bs, &bmap, tl.g0 + (int)rank * 128, r, bar);
-                        tc::tma_2d_pair(Bs + kPanel, &bmap, tl.g0 + (int)rank * 128 + 64, r, bar);
+                        tc::tma_2d_pair(Bs, &bmap, gc, r, bar);
+                        tc::tma_2d_pair(Bs + kPanel, &bmap, gc + 64, r, bar);
                     } else {
                         if (MODE == kGroupedForward) {
                             tc::tma_3d_pair(As, &amap, s * 64, f, tl.e, bar);
@@ -254,42 +267,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                                 tc::tma_2d_pair(Bs + i * 32 * 128, &bmap_s, s * 64, brow + i * 32, bar);
                     }
                 }
+                __syncwarp();
+                if (++st == kGroupedStages) {
+                    st = 0;
+                    phase ^= 1;
+                    filled = true;
+                }
             }
-            if (!ok) tc::settle();
         }
+        if (!ok) tc::settle();
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            // ======================= MMA issuer
+        if (rank == 0) {
+            // ======================= MMA issuer (the whole warp walks, one lane issues)
+            const bool one = tc::elect_one();
+            // descriptors of stage 0, A and B; a stage or a 16-wide step further is an addition to the address
+            const uint32_t a0 = smem_addr(smem), b0 = a0 + kHalfTile;
+            const uint64_t adesc = MODE == kGroupedForward ? tc::sdesc(a0) : tc::sdesc_mn(a0, kPanel);
+            const uint64_t bdesc = WG ? tc::sdesc_mn(b0, kPanel) : tc::sdesc(b0);
+            constexpr uint32_t kA16 = (MODE == kGroupedForward ? 32 : 2048) >> 4, kB16 = (WG ? 2048 : 32) >> 4;
             bool ok = true;
-            int j = 0, it = 0;
-            for (int64_t t = pair; t < total && ok; t += pairs) {
+            int st = 0, it = 0;
+            uint32_t phase = 0;
+            for (int t = pair; t < total && ok; t += pairs) {
                 const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
                 const int KS = WG ? (tl.n + 63) >> 6 : KC;
                 const uint32_t idesc = tc::idesc_f16_major(256, WG ? 256 : (tl.n + 31) & ~31, g.bf16 != 0,
                                                            MODE != kGroupedForward, WG);
-                for (int s = 0; s < KS; ++s, ++j) {
-                    const int st = j % kGroupedStages, ps = OUT32 ? s % kPartSteps : s;
-                    if (ps == 0) {  // a new part: the next accumulator, once the epilogue has drained it
-                        if (it > 1) ok = tc::bar_wait_cluster(&acce_bar[it & 1], ((it >> 1) - 1) & 1, g.status);
+                for (int s = 0; s < KS; ++s) {
+                    const int ps = OUT32 ? s % kPartSteps : s;
+                    if (ps == 0 && it > 1) {  // a new part: the next accumulator, once the epilogue has drained it
+                        ok = tc::bar_wait_cluster(&acce_bar[it & 1], ((it >> 1) - 1) & 1, g.status);
                         if (!ok) break;
-                        tc::fence_after();
                     }
-                    const uint32_t acc_addr = tmem + (it & 1) * 256;
                     // (a cleared step is released by a thread of the other CTA, any other by copies alone)
-                    if (WG && s == KS - 1 && (tl.n & 15)) ok = tc::bar_wait_cluster(&full_bar[st], (j / kGroupedStages) & 1, g.status);
-                    else ok = tc::bar_wait(&full_bar[st], (j / kGroupedStages) & 1, g.status);
+                    if (WG && s == KS - 1 && (tl.n & 15)) ok = tc::bar_wait_cluster(&full_bar[st], phase, g.status);
+                    else ok = tc::bar_wait(&full_bar[st], phase, g.status);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t a_addr = smem_addr(smem + st * kGroupedStage), b_addr = a_addr + kHalfTile;
+                    const uint32_t acc = tmem + (it & 1) * 256;
+                    const uint64_t ad = adesc + (uint32_t)(st * (kGroupedStage >> 4)), bd = bdesc + (uint32_t)(st * (kGroupedStage >> 4));
                     const int kks = WG && s == KS - 1 ? (tl.n - s * 64 + 15) >> 4 : 4;
-                    for (int kk = 0; kk < kks; ++kk) {
-                        const uint64_t ad = MODE == kGroupedForward ? tc::sdesc(a_addr + kk * 32)
-                                                                    : tc::sdesc_mn(a_addr + kk * 2048, kPanel);
-                        const uint64_t bd = WG ? tc::sdesc_mn(b_addr + kk * 2048, kPanel) : tc::sdesc(b_addr + kk * 32);
-                        tc::mma_pair(acc_addr, ad, bd, idesc, (ps > 0 || kk > 0) ? 1u : 0u);
+                    const bool done = s == KS - 1 || (OUT32 && ps == kPartSteps - 1);
+                    if (one) {
+                        tc::mma_pair(acc, ad, bd, idesc, ps > 0 ? 1u : 0u);
+#pragma unroll
+                        for (int kk = 1; kk < 4; ++kk)
+                            if (!WG || kk < kks) tc::mma_pair(acc, ad + kk * kA16, bd + kk * kB16, idesc, 1u);
+                        tc::commit_pair(&empty_bar[st]);
+                        if (done) tc::commit_pair(&accf_bar[it & 1]);
                     }
-                    tc::commit_pair(&empty_bar[st]);
-                    if (s == KS - 1 || (OUT32 && ps == kPartSteps - 1)) tc::commit_pair(&accf_bar[it++ & 1]);
+                    __syncwarp();
+                    if (done) ++it;
+                    if (++st == kGroupedStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok) tc::settle();
@@ -299,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true;
         int j = 0;
         uint32_t phases = 0;  // per stage: parity of its next cleared step
-        for (int64_t t = pair; t < total && ok; t += pairs) {
+        for (int t = pair; t < total && ok; t += pairs) {
             const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
             const int KS = (tl.n + 63) >> 6;
             j += KS;
@@ -329,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         const bool bf16 = g.bf16 != 0;
         float* block = reinterpret_cast<float*>(smem + kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + q * kBlockBytes);
         if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
-        for (int64_t t = pair; t < total && ok; t += pairs) {
+        for (int t = pair; t < total && ok; t += pairs) {
             const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
             const bool empty = WG && tl.n == 0;
             if (empty && g.accumulate) continue;

@@ -149,6 +149,15 @@ MOE_DEV bool bar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status) 
     flag_status(status, kStatusTimeout);
     return false;
 }
+// One lane of a converged warp, the same at every call.  The branch that this
+// predicate guards keeps its operands in uniform registers, which the issue of
+// MMAs and tensor copies reads; under `lane == 0` each operand is moved there
+// first (measured: 160 against ~60 cycles per MMA).
+MOE_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 // After a wait gave up: time for the copies and MMAs in flight to land before
 // shared and tensor memory are released (bounded, about 2 ms).
 MOE_DEV void settle() {

@@ -45,9 +45,11 @@ constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
 // with adapters the epilogue's warps also hold an fp32 block each, in place of the sixth step
-constexpr int grouped_stages(bool adapt) { return adapt ? 5 : 6; }
-constexpr int grouped_smem(bool adapt) {
-    return grouped_stages(adapt) * kGroupedStage + 4 * kEpiWarpBytes + (adapt ? 4 * kBlockBytes : 0) + 1024;
+// (weights: two buffers a warp, so that a tile store reads one while the other is filled)
+constexpr int grouped_stages(int mode, bool adapt) { return adapt || mode == kGroupedWeights ? 5 : 6; }
+constexpr int grouped_smem(int mode, bool adapt) {
+    return grouped_stages(mode, adapt) * kGroupedStage + (mode == kGroupedWeights ? 8 : 4) * kEpiWarpBytes +
+           (adapt ? 4 * kBlockBytes : 0) + 1024;
 }
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
@@ -56,10 +58,10 @@ constexpr int kGroupedMaxGroups = 1024;
 // many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
 // by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
 constexpr int kPartSteps = 8;
-static_assert(grouped_smem(false) + 8 * (kGroupedMaxGroups + 8) <= 227 * 1024, "shared memory");
+static_assert(grouped_smem(kGroupedForward, false) + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
 
 struct GroupedMaps {
-    CUtensorMap a, b, b_small;
+    CUtensorMap a, b, c;  // c: forward and rows, b in 32-row boxes; weights, the result
 };
 
 // 16-bit pair in the requested type
@@ -90,37 +92,55 @@ struct GroupedTile {
     int f0, g0;      // first feature (of the pair); weights: first k column
 };
 
-// The tile list: forward and rows products enumerate (group, 256-row block)
-// by a prefix sum over the groups, features innermost, so the CTAs that run
-// together share the group's rows and its matrix through L2.
+// The tile list.  Forward and rows products cut a group into blocks of equal
+// size (at most 256 rows, multiples of 32, so that no block is a sliver) and
+// enumerate (group, block, features), features innermost: the CTAs that run
+// together share a group's rows and its matrix through L2.  The weight gradient
+// enumerates (group, k columns, features).
+struct TileList {
+    const int* start;  // [E + 1] first row of each group
+    const int* pre;    // [E + 1] forward, rows: blocks of the groups before this place
+    const int* order;  // [E] group at each place
+};
+
+// rows of each block of a group of c rows
+MOE_DEV int block_rows(int c) {
+    const int blocks = (c + 255) >> 8;
+    return blocks <= 1 ? c : (((c + blocks - 1) / blocks) + 31) & ~31;
+}
+
 template <int MODE>
-MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const int* start, const int* pre, int JT) {
+MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const TileList& l, int JT) {
     GroupedTile r;
     if (MODE == kGroupedWeights) {
         const int per = JT * ((g.C + 255) >> 8);
-        r.e = t / per;
-        const int in = t - r.e * per;
+        const int place = t / per, in = t - place * per;
+        r.e = l.order[place];
         r.f0 = (in % JT) << 8;
         r.g0 = (in / JT) << 8;
-        r.row0 = start[r.e];
-        r.n = pre[r.e];
+        r.row0 = l.start[r.e];
+        r.n = l.start[r.e + 1] - r.row0;
         return r;
     }
     const int q = t / JT;
     r.f0 = (t - q * JT) << 8;
     r.g0 = 0;
-    int lo = 0, hi = g.E - 1;  // last group with pre <= q
+    int lo = 0, hi = g.E - 1;  // last place with pre <= q
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= q) lo = mid;
+        if (l.pre[mid] <= q) lo = mid;
         else hi = mid - 1;
     }
-    r.e = lo;
-    const int first = start[lo] + ((q - pre[lo]) << 8);
-    r.row0 = first;
-    r.n = min(256, start[lo + 1] - first);
+    r.e = l.order[lo];
+    const int c = l.start[r.e + 1] - l.start[r.e], rows = block_rows(c), at = (q - l.pre[lo]) * rows;
+    r.row0 = l.start[r.e] + at;
+    r.n = min(rows, c - at);
     return r;
 }
+
+// The i-th tile of pair p of P, back and forth over the pairs: with costs that
+// fall along the list every pair gets about the same sum.
+MOE_DEV int tile_index(int i, int p, int P) { return i * P + ((i & 1) ? P - 1 - p : p); }
 
 // Exclusive scan (sum, or running maximum from `start`) of one value per thread
 // over the CTA; every thread calls it.
@@ -147,14 +167,14 @@ MOE_DEV int block_exclusive(int v, int start, int* wsum) {
 template <int MODE, bool OUT32, bool ADAPT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     grouped_kernel(const GroupedArgs g, const AdapterArgs ad, const __grid_constant__ CUtensorMap amap,
-                   const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap bmap_s) {
+                   const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap) {
     constexpr bool WG = MODE == kGroupedWeights;
-    constexpr int kGroupedStages = grouped_stages(ADAPT);
+    constexpr int kGroupedStages = grouped_stages(MODE, ADAPT);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[kGroupedStages], empty_bar[kGroupedStages], tail_bar[kGroupedStages];
     __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ int start[kGroupedMaxGroups + 1], pre[kGroupedMaxGroups + 1];
+    __shared__ int start[kGroupedMaxGroups + 1], pre[WG ? 1 : kGroupedMaxGroups + 1], order[kGroupedMaxGroups];
     __shared__ int wsum[kGroupedThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -176,8 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     if (warp == 2) tc::tmem_alloc_pair(&tmem_slot, 512);
 
     // Group starts: clamped into [0, rows] and made ascending by a running
-    // maximum, so that a bad table reads and writes nothing out of range; pre =
-    // prefix sum of the groups' 256-row blocks, or (weights) each group's rows.
+    // maximum, so that a bad table reads and writes nothing out of range.
     constexpr int kPer = kGroupedMaxGroups / kGroupedThreads;
     const int first = ADAPT ? 0 : min(max(__ldg(&g.offsets[0]), 0), g.M);
     int end[kPer], top = first;
@@ -188,32 +207,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         end[i] = top;
     }
     const int top_before = block_exclusive<true>(top, first, wsum);
-    int begin = max(top_before, first), mine = 0, blocks[kPer];
+    int begin = max(top_before, first);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i, stop = max(end[i], begin);
-        if (e < g.E) start[e] = begin;
+        if (e < g.E) {
+            start[e] = begin;
+            // the sort key: rows of one tile
+            order[e] = WG ? stop - begin : block_rows(stop - begin);
+        }
         if (e == g.E - 1) start[g.E] = stop;
-        if (WG && e < g.E) pre[e] = stop - begin;
-        blocks[i] = e < g.E ? (stop - begin + 255) >> 8 : 0;
-        mine += blocks[i];
         begin = stop;
     }
+    __syncthreads();
+    // Places by falling tile cost, so that the long tiles come first and the
+    // pairs end together.  Where the groups are so small that reading their
+    // matrices is the cost (under 256 rows on average), the groups' own order,
+    // which mixes short and long tiles and keeps HBM busy throughout.
+    int place[kPer];
+    const bool sorted = !ADAPT && (WG || start[g.E] - start[0] >= 256 * g.E);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        place[i] = e;
+        if (sorted && e < g.E) {
+            const int key = order[e];
+            int n = 0;
+            for (int o = 0; o < g.E; ++o) {
+                const int k = order[o];
+                n += k > key || (k == key && o < e);
+            }
+            place[i] = n;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (tid * kPer + i < g.E) order[place[i]] = tid * kPer + i;
+    __syncthreads();
     int total;
     if (WG) {
         total = g.E * JT * ((g.C + 255) >> 8);
     } else {
+        int mine = 0, blocks[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = tid * kPer + i;
+            const int e = at < g.E ? order[at] : 0;
+            blocks[i] = at < g.E ? (start[e + 1] - start[e] + 255) >> 8 : 0;
+            mine += blocks[i];
+        }
         int before = block_exclusive<false>(mine, 0, wsum);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int e = tid * kPer + i;
-            if (e < g.E) pre[e] = before;
+            const int at = tid * kPer + i;
+            if (at < g.E) pre[at] = before;
             before += blocks[i];
-            if (e == g.E - 1) pre[g.E] = before;
+            if (at == g.E - 1) pre[g.E] = before;
         }
         __syncthreads();
         total = pre[g.E] * JT;
     }
+    const TileList list{start, pre, order};
     tc::fence_before();
     __syncthreads();
     tc::cluster_sync();  // both CTAs' barriers are initialised, both halves of tensor memory allocated
@@ -229,8 +284,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true, filled = false;  // filled: every stage has been used once
         int st = 0;
         uint32_t phase = 1;  // parity of the stage's last "empty" (0 once every stage has been used)
-        for (int t = pair; t < total && ok; t += pairs) {
-            const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+        for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
+            const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
             const int KS = WG ? (tl.n + 63) >> 6 : KC;
             const int nh = WG ? 128 : ((tl.n + 31) & ~31) >> 1;
             const int brow = tl.row0 + (int)rank * nh;
@@ -264,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         if (nbox == 0) tc::tma_2d_pair(Bs, &bmap, s * 64, brow, bar);
                         else
                             for (int i = 0; i < nbox; ++i)
-                                tc::tma_2d_pair(Bs + i * 32 * 128, &bmap_s, s * 64, brow + i * 32, bar);
+                                tc::tma_2d_pair(Bs + i * 32 * 128, &cmap, s * 64, brow + i * 32, bar);
                     }
                 }
                 __syncwarp();
@@ -288,8 +343,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             bool ok = true;
             int st = 0, it = 0;
             uint32_t phase = 0;
-            for (int t = pair; t < total && ok; t += pairs) {
-                const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+            for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
+                const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
                 const int KS = WG ? (tl.n + 63) >> 6 : KC;
                 const uint32_t idesc = tc::idesc_f16_major(256, WG ? 256 : (tl.n + 31) & ~31, g.bf16 != 0,
                                                            MODE != kGroupedForward, WG);
@@ -331,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true;
         int j = 0;
         uint32_t phases = 0;  // per stage: parity of its next cleared step
-        for (int t = pair; t < total && ok; t += pairs) {
-            const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+        for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
+            const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
             const int KS = (tl.n + 63) >> 6;
             j += KS;
             if (!(tl.n & 15)) continue;
@@ -355,14 +410,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     } else if (warp >= 4) {
         // ======================= epilogue: lane = feature, register = column
         const int q = warp & 3;
-        uint8_t* stg = smem + kGroupedStages * kGroupedStage + q * kEpiWarpBytes;
+        uint8_t* stg = smem + kGroupedStages * kGroupedStage + q * (WG ? 2 : 1) * kEpiWarpBytes;
+        const bool one = tc::elect_one();
         bool ok = true;
         int it = 0;
         const bool bf16 = g.bf16 != 0;
         float* block = reinterpret_cast<float*>(smem + kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + q * kBlockBytes);
         if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
-        for (int t = pair; t < total && ok; t += pairs) {
-            const GroupedTile tl = tile_at<MODE>(g, t, start, pre, JT);
+        for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
+            const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
             const bool empty = WG && tl.n == 0;
             if (empty && g.accumulate) continue;
             const int KS = WG ? (tl.n + 63) >> 6 : KC;
@@ -434,54 +490,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         if (more) tc::ld_wait();
                     }
                 } else {
-                    // 128 bytes of each of the warp's 32 rows at a time, 16-byte pieces permuted against bank conflicts
-                    constexpr int kCols = OUT32 ? 32 : 64, kVec = OUT32 ? 4 : 8;
-                    for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
-                        if (empty) {
-#pragma unroll
-                            for (int p = 0; p < 8; ++p)
-                                *reinterpret_cast<uint4*>(stg + lane * 128 + p * 16) = make_uint4(0, 0, 0, 0);
-                        } else {
+                    // 32 features x 128 bytes at a time, through two swizzled buffers and tile stores (which
+                    // clip at the matrix's edges).  Later parts, and MOE_ACCUMULATE, are added in L2 by the
+                    // store itself, each part once the one before has landed: a fixed order of additions
+                    constexpr int kCols = OUT32 ? 32 : 64;
+                    if (part > 0) {
+                        if (one) tc::store_wait_done();
+                        __syncwarp();
+                    }
+                    if (f < g.F) {
+                        for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
+                            uint32_t r[32];
+                            uint8_t* buf = stg + ((c0 / kCols) & 1) * kEpiWarpBytes;
+                            if (!empty) {
+                                tc::ld16_nowait(tb + c0, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                                tc::ld16_nowait(tb + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                            }
+                            if (one) tc::store_wait_read<1>();
+                            __syncwarp();
 #pragma unroll
                             for (int h = 0; h < kCols; h += 32) {
-                                uint32_t r[32];
-                                tc::ld16_nowait(tb + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-                                tc::ld16_nowait(tb + c0 + h + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
-                                tc::ld_wait();
-#pragma unroll
-                                for (int p = 0; p < 32 / kVec; ++p) {
-                                    uint4 v;
-                                    if (OUT32) {
-                                        v = make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
-                                    } else {
-                                        uint32_t w[4];
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i)
-                                            w[i] = pack16(__uint_as_float(r[(8 * p + 2 * i) & 31]),
-                                                          __uint_as_float(r[(8 * p + 2 * i + 1) & 31]), bf16);
-                                        v = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (!empty) {
+                                    if (h) {
+                                        tc::ld16_nowait(tb + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                                        tc::ld16_nowait(tb + c0 + h + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
                                     }
-                                    const int piece = h / kVec + p;
-                                    *reinterpret_cast<uint4*>(stg + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+                                    tc::ld_wait();
                                 }
-                            }
-                        }
-                        __syncwarp();
-                        const int col = tl.g0 + c0 + (lane & 7) * kVec;
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) {
-                            const int row = p * 4 + (lane >> 3);
-                            if (f + row < g.F && col < g.C) {
-                                uint4 v = *reinterpret_cast<const uint4*>(stg + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                                const int64_t o = ((int64_t)tl.e * g.F + f + row) * g.ldo + col;
-                                if (OUT32) {
-                                    add_store(static_cast<float*>(g.out) + o, v, add);
-                                } else {
-                                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + o) = v;
+                                for (int p = 0; p < (OUT32 ? 8 : 4); ++p) {
+                                    uint4 v = make_uint4(0, 0, 0, 0);
+                                    if (!empty) {
+                                        if (OUT32) {
+                                            v = make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
+                                        } else {
+                                            uint32_t w[4];
+#pragma unroll
+                                            for (int i = 0; i < 4; ++i)
+                                                w[i] = pack16(__uint_as_float(r[(8 * p + 2 * i) & 31]),
+                                                              __uint_as_float(r[(8 * p + 2 * i + 1) & 31]), bf16);
+                                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                                        }
+                                    }
+                                    const int piece = h / 8 + p;
+                                    *reinterpret_cast<uint4*>(buf + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
                                 }
                             }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (one) {
+                                if (add) tc::add_3d(&cmap, tl.g0 + c0, f, tl.e, buf);
+                                else tc::store_3d(&cmap, tl.g0 + c0, f, tl.e, buf);
+                                tc::store_commit();
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 }
                 if (!empty) {
@@ -491,6 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 }
             }
         }
+        if (WG && one) tc::store_wait_done();
         if (!ok) tc::settle();
     }
     tc::fence_before();
@@ -509,21 +573,22 @@ static int sm_count() {
 }
 
 // map of a row-major 16-bit matrix [rows x cols], rows `ld` values apart; boxes of 64 columns x box_rows
+static Elem elem16(bool bf16) { return bf16 ? Elem::kBf16 : Elem::kFp16; }
 static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld,
                           int box_rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, str[1] = {(cuuint64_t)ld * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    return encode_sw128(m, bf16, base, 2, dims, str, box);
+    return encode_sw128(m, elem16(bf16), base, 2, dims, str, box);
 }
 
 template <int MODE, bool OUT32>
 static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
     auto kern = grouped_kernel<MODE, OUT32, false>;
-    constexpr int smem = grouped_smem(false);
+    constexpr int smem = grouped_smem(MODE, false);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
-    kern<<<2 * pairs, kGroupedThreads, smem, s>>>(g, AdapterArgs{}, m.a, m.b, m.b_small);
+    kern<<<2 * pairs, kGroupedThreads, smem, s>>>(g, AdapterArgs{}, m.a, m.b, m.c);
     return cudaGetLastError();
 }
 
@@ -533,9 +598,9 @@ static cudaError_t product_maps(GroupedMaps* m, bool forward, bool bf, int E, in
     const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
     const cuuint64_t str[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
     const cuuint32_t box[3] = {64, forward ? 128u : 64u, 1};
-    cudaError_t e = encode_sw128(&m->a, bf, w, 3, dims, str, box);
+    cudaError_t e = encode_sw128(&m->a, elem16(bf), w, 3, dims, str, box);
     if (e == cudaSuccess) e = map_2d(&m->b, bf, rows, M, forward ? K : N, ld, 128);
-    if (e == cudaSuccess) e = map_2d(&m->b_small, bf, rows, M, forward ? K : N, ld, 32);
+    if (e == cudaSuccess) e = map_2d(&m->c, bf, rows, M, forward ? K : N, ld, 32);
     return e;
 }
 
@@ -555,7 +620,7 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     g.accumulate = p.accumulate;
     g.status = p.status;
     auto kern = grouped_kernel<kGroupedForward, OUT32, true>;
-    constexpr int smem = grouped_smem(true);
+    constexpr int smem = grouped_smem(kGroupedForward, true);
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256);
@@ -569,7 +634,7 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, g, p, m.a, m.b, m.b_small);
+    return cudaLaunchKernelEx(&cfg, kern, g, p, m.a, m.b, m.c);
 }
 
 cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {
@@ -585,8 +650,12 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const 
     if (mode == kGroupedWeights) {
         e = map_2d(&m.a, bf, dy, g.M, g.F, lddy, 64);
         if (e == cudaSuccess) e = map_2d(&m.b, bf, x, g.M, g.C, ldx, 64);
+        const int bytes = out_fp32 ? 4 : 2;
+        const cuuint64_t dims[3] = {(cuuint64_t)g.C, (cuuint64_t)g.F, (cuuint64_t)g.E};
+        const cuuint64_t str[2] = {(cuuint64_t)g.C * bytes, (cuuint64_t)g.F * g.C * bytes};
+        const cuuint32_t box[3] = {(cuuint32_t)(128 / bytes), 32, 1};
+        if (e == cudaSuccess) e = encode_sw128(&m.c, out_fp32 ? Elem::kFp32 : elem16(bf), g.out, 3, dims, str, box);
         if (e != cudaSuccess) return e;
-        m.b_small = m.b;
         const int64_t tiles = (int64_t)g.E * JT * ((g.C + 255) / 256);
         return out_fp32 ? grouped_launch<kGroupedWeights, true>(g, m, tiles, s)
                         : grouped_launch<kGroupedWeights, false>(g, m, tiles, s);

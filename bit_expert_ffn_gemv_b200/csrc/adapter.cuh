@@ -109,14 +109,11 @@ MOE_DEV void adapter_delta(const AdapterArgs& p, int t0, uint32_t used, int a, i
     }
 }
 
-// The 16 x 32 fp32 block of a warp in shared memory, [token][feature].
-constexpr int kBlockPitch = 36;  // floats: fragments and rows are both free of bank conflicts
-constexpr int kBlockBytes = 16 * kBlockPitch * 4;
-
-// block[token][feature] += delta for the tokens t0 .. t0 + n - 1 (n <= 16),
-// whole warps; any order of ids.  One pass per distinct adapter of the 16.
+// Adds the delta of tokens t0 .. t0 + n - 1 (n <= 16) to the fragments lo
+// (features f0 .. f0 + 15) and hi (f0 + 16 .. f0 + 31): two of 8 tokens each,
+// fp32 bits.  Whole warps; any order of ids, one pass per distinct adapter.
 template <bool BF16, int TERMS>
-MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int f0, float* block) {
+MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int f0, uint32_t* lo, uint32_t* hi) {
     const int lane = threadIdx.x & 31;
     int id = lane < n ? __ldg(&p.ids[t0 + lane]) : -1;
     if (id < 0 || id >= p.L) id = -1;
@@ -130,16 +127,14 @@ MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int f0, float* block
         DeltaFrags fr;
         adapter_delta<BF16, TERMS>(p, t0, used, a, f0, fr);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = frag_token(q, i);
-                    // (another adapter's infinities must not reach this token)
-                    if ((used >> t) & 1) block[t * kBlockPitch + frag_feature(m, i)] += fr.d[m][q][i];
-                }
-        __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+                // (another adapter's infinities must not reach this token)
+                if (!((used >> frag_token(q, i)) & 1)) continue;
+                lo[4 * q + i] = __float_as_uint(__uint_as_float(lo[4 * q + i]) + fr.d[0][q][i]);
+                hi[4 * q + i] = __float_as_uint(__uint_as_float(hi[4 * q + i]) + fr.d[1][q][i]);
+            }
     }
 }
 

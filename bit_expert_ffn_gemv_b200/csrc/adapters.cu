@@ -125,38 +125,40 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArg
 }
 
 // ---------------------------------------------------------------- the delta alone
-// CTA: 128 features (32 a warp) by 32 tokens, 16 at a time.
+// CTA: 128 features (32 a warp) by 32 tokens, 16 at a time, in fragments.
 template <bool BF16, bool OUT32>
 __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
-    __shared__ __align__(16) float blocks[4][kBlockBytes / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int f0 = blockIdx.x * 128 + warp * 32;
-    float* block = blocks[warp];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (f0 >= p.N) return;
     const int end = min(p.T, ((int)blockIdx.y + 1) * 32);
     for (int t0 = blockIdx.y * 32; t0 < end; t0 += 16) {
         const int n = min(16, end - t0);
-        const bool in = f0 + lane < p.N;
-        __syncwarp();
+        uint32_t r[2][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = 0.f;
-            if (p.accumulate && i < n && in) {
-                const int64_t o = (int64_t)(t0 + i) * p.ldy + f0 + lane;
-                v = OUT32 ? static_cast<const float*>(p.y)[o] : unpack1<BF16>(static_cast<const uint16_t*>(p.y)[o]);
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = frag_token(i >> 2, i), f = f0 + frag_feature(m, i & 3);
+                float v = 0.f;
+                if (p.accumulate && t < n && f < p.N) {
+                    const int64_t o = (int64_t)(t0 + t) * p.ldy + f;
+                    v = OUT32 ? static_cast<const float*>(p.y)[o] : unpack1<BF16>(static_cast<const uint16_t*>(p.y)[o]);
+                }
+                r[m][i] = __float_as_uint(v);
             }
-            block[i * kBlockPitch + lane] = v;
-        }
-        __syncwarp();
-        add_delta<BF16, BF16 && OUT32 ? 3 : 2>(p, t0, n, f0, block);
+        add_delta<BF16, BF16 && OUT32 ? 3 : 2>(p, t0, n, f0, r[0], r[1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < n && in) {
-                const int64_t o = (int64_t)(t0 + i) * p.ldy + f0 + lane;
-                const float v = block[i * kBlockPitch + lane];
-                if (OUT32) static_cast<float*>(p.y)[o] = v;
-                else static_cast<uint16_t*>(p.y)[o] = pack1<BF16>(v);
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = frag_token(i >> 2, i), f = f0 + frag_feature(m, i & 3);
+                if (t < n && f < p.N) {
+                    const int64_t o = (int64_t)(t0 + t) * p.ldy + f;
+                    if (OUT32) static_cast<float*>(p.y)[o] = __uint_as_float(r[m][i]);
+                    else static_cast<uint16_t*>(p.y)[o] = pack1<BF16>(__uint_as_float(r[m][i]));
+                }
             }
     }
 }

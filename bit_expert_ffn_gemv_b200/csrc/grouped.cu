@@ -44,12 +44,11 @@ constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an
 constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
-// with adapters the epilogue's warps also hold an fp32 block each, in place of the sixth step
 // (weights: two buffers a warp, so that a tile store reads one while the other is filled)
-constexpr int grouped_stages(int mode, bool adapt) { return adapt || mode == kGroupedWeights ? 5 : 6; }
-constexpr int grouped_smem(int mode, bool adapt) {
-    return grouped_stages(mode, adapt) * kGroupedStage + (mode == kGroupedWeights ? 8 : 4) * kEpiWarpBytes +
-           (adapt ? 4 * kBlockBytes : 0) + 1024;
+constexpr int grouped_stages(int mode) { return mode == kGroupedWeights ? 5 : 6; }
+constexpr int grouped_smem(int mode) {
+    return grouped_stages(mode) * kGroupedStage + (mode == kGroupedWeights ? 8 : 4) * kEpiWarpBytes +
+           1024;
 }
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
@@ -58,7 +57,7 @@ constexpr int kGroupedMaxGroups = 1024;
 // many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
 // by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
 constexpr int kPartSteps = 8;
-static_assert(grouped_smem(kGroupedForward, false) + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
+static_assert(grouped_smem(kGroupedForward) + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
 
 struct GroupedMaps {
     CUtensorMap a, b, c;  // c: forward and rows, b in 32-row boxes; weights, the result
@@ -77,15 +76,8 @@ MOE_DEV uint16_t to16(float v, bool bf16) {
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
-// four fp32 values at p, or added to those there (the same thread wrote them)
-MOE_DEV void add_store(float* p, const uint4& v, bool add) {
-    float4 s = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-    if (add) {
-        const float4 was = *reinterpret_cast<const float4*>(p);
-        s = make_float4(was.x + s.x, was.y + s.y, was.z + s.z, was.w + s.w);
-    }
-    *reinterpret_cast<float4*>(p) = s;
-}
+// *p += v without waiting for the old value (one thread owns p: its additions keep their order)
+MOE_DEV void add_global(float* p, float v) { asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
 
 struct GroupedTile {
     int e, row0, n;  // group; first row and rows of the tile (weights: of the group)
@@ -169,7 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     grouped_kernel(const GroupedArgs g, const AdapterArgs ad, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap) {
     constexpr bool WG = MODE == kGroupedWeights;
-    constexpr int kGroupedStages = grouped_stages(MODE, ADAPT);
+    constexpr int kGroupedStages = grouped_stages(MODE);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[kGroupedStages], empty_bar[kGroupedStages], tail_bar[kGroupedStages];
     __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
@@ -398,11 +390,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             if (!ok) break;
             phases ^= 1u << st;
             const int r0 = tl.n - (KS - 1) * 64, nz = ((r0 + 15) & ~15) - r0;
-            uint8_t* base = smem + st * kGroupedStage + r0 * 128;
-            for (int i = lane; i < 4 * nz * 8; i += 32) {
-                const int p = i / (nz * 8), c = i - p * nz * 8;
-                *reinterpret_cast<uint4*>(base + p * kPanel + c * 16) = make_uint4(0, 0, 0, 0);
-            }
+            // 4 panels x 8 pieces: a row a turn
+            uint8_t* base = smem + st * kGroupedStage + (lane >> 3) * kPanel + r0 * 128 + (lane & 7) * 16;
+            for (int i = 0; i < nz; ++i) *reinterpret_cast<uint4*>(base + i * 128) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&full_bar[st], 0));
@@ -415,7 +405,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true;
         int it = 0;
         const bool bf16 = g.bf16 != 0;
-        float* block = reinterpret_cast<float*>(smem + kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + q * kBlockBytes);
         if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
         for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
             const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
@@ -436,58 +425,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + b * 256;
                 const int f = tl.f0 + (int)rank * 128 + 32 * q;  // the warp's first feature
                 if (!WG) {
-                    // 16 rows at a time: [row][32 features] in shared memory, then whole 16-byte pieces of the rows
-                    constexpr int kVec = OUT32 ? 4 : 8, kSegs = 32 / kVec, kRowsPer = 32 / kSegs;
-                    const int seg = lane % kSegs, vr = lane / kSegs;
-                    const bool in = f + seg * kVec < g.F;
-                    const int64_t at = (int64_t)tl.row0 * g.ldo + f + seg * kVec;
-                    uint32_t r[16];
-                    tc::ld16_nowait(tb, r);
+                    // 32 rows at a time.  TMEM is read as warp-MMA fragments, so an adapter's delta is added in
+                    // registers; 16-bit results are packed in pairs and transposed by stmatrix into [row][32
+                    // features] (16-byte pieces permuted against bank conflicts), then leave as whole pieces of
+                    // the rows.  fp32 results leave from the fragments: 8 lanes fill a 32-byte sector
+                    const int seg = lane & 3, vr = lane >> 2;
+                    const bool in = f + seg * 8 < g.F;
+                    const int64_t at = (int64_t)tl.row0 * g.ldo + f;
+                    // stmatrix: this lane's row of matrix lane / 8: token, 16-byte piece
+                    const int mrow = (lane & 7) + 8 * (lane >> 4), mpiece = (lane >> 3) & 1;
+                    uint32_t r[2][16];  // [16 features][fragment of 8 rows]
+                    tc::ld_frags_nowait(tb, r[0]);
+                    tc::ld_frags_nowait(tb + (16u << 16), r[1]);
                     tc::ld_wait();
-                    for (int c0 = 0; c0 < tl.n; c0 += 16) {
-                        if (ADAPT && part == 0) {  // the delta, through the fp32 block and back
-                            const int m = min(16, tl.n - c0);
+                    for (int c0 = 0; c0 < tl.n; c0 += 32) {
+                        if (ADAPT && part == 0) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) block[i * kBlockPitch + lane] = __uint_as_float(r[i]);
-                            __syncwarp();
-                            if (bf16) add_delta<true, OUT32 ? 3 : 2>(ad, tl.row0 + c0, m, f, block);
-                            else add_delta<false, 2>(ad, tl.row0 + c0, m, f, block);
-                            __syncwarp();
+                            for (int h = 0; h < 2; ++h)
+                                if (c0 + 16 * h < tl.n) {
+                                    const int m = min(16, tl.n - c0 - 16 * h);
+                                    if (bf16) add_delta<true, OUT32 ? 3 : 2>(ad, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
+                                    else add_delta<false, 2>(ad, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
+                                }
+                        }
+                        if (ADAPT && !OUT32 && g.accumulate) {  // y's values, added before the one rounding
+                            const uint16_t* y = static_cast<const uint16_t*>(g.out) + at + (int64_t)c0 * g.ldo;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(block[i * kBlockPitch + lane]);
-                            if (!OUT32 && g.accumulate && f + lane < g.F) {
-                                const uint16_t* y = static_cast<const uint16_t*>(g.out) + (int64_t)(tl.row0 + c0) * g.ldo + f + lane;
+                            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (i < m) {
-                                        const uint16_t was = y[(int64_t)i * g.ldo];
-                                        r[i] = __float_as_uint(__uint_as_float(r[i]) + (bf16 ? unpack1<true>(was) : unpack1<false>(was)));
+                                for (int i = 0; i < 16; ++i) {
+                                    const int row = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                                    const int ff = 16 * m + (lane >> 2) + 8 * ((i >> 1) & 1);
+                                    if (c0 + row < tl.n && f + ff < g.F) {
+                                        const uint16_t was = y[(int64_t)row * g.ldo + ff];
+                                        r[m][i] = __float_as_uint(__uint_as_float(r[m][i]) +
+                                                                  (bf16 ? unpack1<true>(was) : unpack1<false>(was)));
                                     }
-                            }
+                                }
                         }
+                        const bool more = c0 + 32 < tl.n;
                         if (OUT32) {
+                            float* out = static_cast<float*>(g.out) + at + (int64_t)c0 * g.ldo;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(stg)[i * 32 + lane] = r[i];
-                        } else {
+                            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                reinterpret_cast<uint16_t*>(stg)[i * 32 + lane] = to16(__uint_as_float(r[i]), bf16);
-                        }
-                        const bool more = c0 + 16 < tl.n;
-                        if (more) tc::ld16_nowait(tb + c0 + 16, r);
-                        __syncwarp();
-#pragma unroll
-                        for (int p = 0; p < 16 / kRowsPer; ++p) {
-                            const int row = p * kRowsPer + vr;
-                            if (in && c0 + row < tl.n) {
-                                const uint4 v = *reinterpret_cast<const uint4*>(stg + row * (OUT32 ? 128 : 64) + seg * 16);
-                                const int64_t o = at + (int64_t)(c0 + row) * g.ldo;
-                                if (OUT32) add_store(static_cast<float*>(g.out) + o, v, add);
-                                else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + o) = v;
+                                for (int i = 0; i < 16; ++i) {
+                                    const int row = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                                    const int ff = 16 * m + (lane >> 2) + 8 * ((i >> 1) & 1);
+                                    if (c0 + row < tl.n && f + ff < g.F) {
+                                        float* p = out + (int64_t)row * g.ldo + ff;
+                                        if (add) add_global(p, __uint_as_float(r[m][i]));
+                                        else *p = __uint_as_float(r[m][i]);
+                                    }
+                                }
+                            if (more) {
+                                tc::ld_frags_nowait(tb + c0 + 32, r[0]);
+                                tc::ld_frags_nowait(tb + (16u << 16) + c0 + 32, r[1]);
+                                tc::ld_wait();
                             }
+                        } else {
+                            uint8_t* buf = stg + ((c0 >> 5) & 1) * 2048;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int n = 0; n < 4; n += 2) {
+                                    const uint32_t* v = &r[m][4 * n];
+                                    const int token = 8 * n + mrow, piece = 2 * m + mpiece;
+                                    tc::stmatrix4_trans(smem_addr(buf) + token * 64 + ((piece ^ ((token >> 1) & 3)) << 4),
+                                                        pack16(__uint_as_float(v[0]), __uint_as_float(v[1]), bf16),
+                                                        pack16(__uint_as_float(v[2]), __uint_as_float(v[3]), bf16),
+                                                        pack16(__uint_as_float(v[4]), __uint_as_float(v[5]), bf16),
+                                                        pack16(__uint_as_float(v[6]), __uint_as_float(v[7]), bf16));
+                                }
+                            if (more) {  // in flight while this block leaves
+                                tc::ld_frags_nowait(tb + c0 + 32, r[0]);
+                                tc::ld_frags_nowait(tb + (16u << 16) + c0 + 32, r[1]);
+                            }
+                            __syncwarp();
+                            uint16_t* out = static_cast<uint16_t*>(g.out) + at + seg * 8;
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const int row = 8 * p + vr;
+                                if (in && c0 + row < tl.n) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 64 + ((seg ^ ((row >> 1) & 3)) << 4));
+                                    uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)(c0 + row) * g.ldo);
+                                    *dst = v;
+                                }
+                            }
+                            if (more) tc::ld_wait();
                         }
-                        __syncwarp();
-                        if (more) tc::ld_wait();
                     }
                 } else {
                     // 32 features x 128 bytes at a time, through two swizzled buffers and tile stores (which
@@ -584,7 +610,7 @@ static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t r
 template <int MODE, bool OUT32>
 static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
     auto kern = grouped_kernel<MODE, OUT32, false>;
-    constexpr int smem = grouped_smem(MODE, false);
+    constexpr int smem = grouped_smem(MODE);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
@@ -620,7 +646,7 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     g.accumulate = p.accumulate;
     g.status = p.status;
     auto kern = grouped_kernel<kGroupedForward, OUT32, true>;
-    constexpr int smem = grouped_smem(kGroupedForward, true);
+    constexpr int smem = grouped_smem(kGroupedForward);
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256);

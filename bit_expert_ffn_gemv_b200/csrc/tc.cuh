@@ -56,10 +56,27 @@ MOE_DEV void ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+// 32 columns of 16 TMEM lanes as four warp-MMA accumulator fragments: r[4 n + i]
+// is lane (row) l / 4 + 8 (i / 2), column 8 n + 2 (l % 4) + i % 2 (no wait)
+MOE_DEV void ld_frags_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 MOE_DEV void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 MOE_DEV void ld16(uint32_t taddr, uint32_t (&r)[16]) {
     ld16_nowait(taddr, r);
     ld_wait();
+}
+
+// four 8x8 16-bit matrices, transposed: lane l gives the address of row l % 8
+// of matrix l / 8; register j is that matrix's fragment
+MOE_DEV void stmatrix4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
 }
 
 MOE_DEV void cp16(void* dst, const void* src) {

@@ -768,8 +768,8 @@ static cudaError_t encode_2d(CUtensorMap* map, CUtensorMapDataType type, int ele
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t encode_sw128(CUtensorMap* map, Elem type, const void* base, int rank, const cuuint64_t* dims,
-                         const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+cudaError_t encode_tiles(CUtensorMap* map, Elem type, const void* base, int rank, const cuuint64_t* dims,
+                         const cuuint64_t* strides_bytes, const cuuint32_t* box, int swizzle_bytes) {
     Encode encode = encoder();
     if (!encode) return cudaErrorNotSupported;
     const cuuint32_t estr[3] = {1, 1, 1};
@@ -777,7 +777,8 @@ cudaError_t encode_sw128(CUtensorMap* map, Elem type, const void* base, int rank
                              : type == Elem::kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                         (cuuint32_t)rank, const_cast<void*>(base), dims, strides_bytes, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

@@ -19,8 +19,9 @@
 // are read MN-major, straight from row-major memory.
 //
 // Warp roles (every role walks the same tile sequence; persistent):
-//   warp 0      loader (one thread): TMA of this CTA's halves into a 6-deep
-//               ring of K = 64 steps, completing on the leader's full[stage]
+//   warps 0, 3  loaders (one lane each): TMA of this CTA's half of A and of B
+//               into a ring of K = 64 steps, completing on the leader's
+//               full[stage]
 //   warp 1      MMA issuer (leader CTA, one thread)
 //   warp 2      tensor-memory allocation; weight gradient: zeroes the rows of
 //               the last step that belong to the next group (a product with
@@ -44,12 +45,8 @@ constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an
 constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
-// (weights: two buffers a warp, so that a tile store reads one while the other is filled)
-constexpr int grouped_stages(int mode) { return mode == kGroupedWeights ? 5 : 6; }
-constexpr int grouped_smem(int mode) {
-    return grouped_stages(mode) * kGroupedStage + (mode == kGroupedWeights ? 8 : 4) * kEpiWarpBytes +
-           1024;
-}
+constexpr int kGroupedStages = 6;
+constexpr int kGroupedSmem = kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + 1024;
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
 // 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
@@ -57,7 +54,7 @@ constexpr int kGroupedMaxGroups = 1024;
 // many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
 // by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
 constexpr int kPartSteps = 8;
-static_assert(grouped_smem(kGroupedForward) + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
+static_assert(kGroupedSmem + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
 
 struct GroupedMaps {
     CUtensorMap a, b, c;  // c: forward and rows, b in 32-row boxes; weights, the result
@@ -161,7 +158,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     grouped_kernel(const GroupedArgs g, const AdapterArgs ad, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap) {
     constexpr bool WG = MODE == kGroupedWeights;
-    constexpr int kGroupedStages = grouped_stages(MODE);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[kGroupedStages], empty_bar[kGroupedStages], tail_bar[kGroupedStages];
     __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
@@ -175,9 +171,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kGroupedStages; ++i) {
-            mbar_init(&full_bar[i], 2);
+            mbar_init(&full_bar[i], 4);
             mbar_init(&empty_bar[i], 1);
-            mbar_init(&tail_bar[i], 1);
+            mbar_init(&tail_bar[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accf_bar[i], 1);
@@ -269,9 +265,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
     const int KC = (g.C + 63) >> 6;  // steps per tile (forward, rows)
 
-    if (warp == 0) {
-        // ======================= loader (the whole warp walks, one lane issues)
-        const bool one = tc::elect_one();
+    if (warp == 0 || warp == 3) {
+        // ======================= loaders (the whole warp walks, one lane issues): warp 0 A, warp 3 B
+        const bool is_a = warp == 0, one = tc::elect_one();
         const uint32_t full_leader = tc::cluster_addr(&full_bar[0], 0), tail_own = tc::cluster_addr(&tail_bar[0], rank);
         bool ok = true, filled = false;  // filled: every stage has been used once
         int st = 0;
@@ -283,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             const int brow = tl.row0 + (int)rank * nh;
             const int f = tl.f0 + (int)rank * 128, gc = tl.g0 + (int)rank * 128;
             const int nbox = nh > 64 ? 0 : (nh + 31) >> 5;  // 32-row boxes (0: one of 128 rows)
-            const uint32_t bytes = kHalfTile + (WG || nbox == 0 ? kHalfTile : nbox * 32 * 128);
+            const uint32_t bytes = is_a || WG || nbox == 0 ? kHalfTile : nbox * 32 * 128;
             for (int s = 0; s < KS; ++s) {
                 if (filled) ok = tc::bar_wait(&empty_bar[st], phase, g.status);
                 if (!ok) break;
@@ -297,21 +293,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     else tc::arrive_expect_cluster(bar, bytes);
                     if (WG) {
                         const int r = tl.row0 + s * 64;
-                        tc::tma_2d_pair(As, &amap, f, r, bar);
-                        tc::tma_2d_pair(As + kPanel, &amap, f + 64, r, bar);
-                        tc::tma_2d_pair(Bs, &bmap, gc, r, bar);
-                        tc::tma_2d_pair(Bs + kPanel, &bmap, gc + 64, r, bar);
-                    } else {
+                        if (is_a) {
+                            tc::tma_2d_pair(As, &amap, f, r, bar);
+                            tc::tma_2d_pair(As + kPanel, &amap, f + 64, r, bar);
+                        } else {
+                            tc::tma_2d_pair(Bs, &bmap, gc, r, bar);
+                            tc::tma_2d_pair(Bs + kPanel, &bmap, gc + 64, r, bar);
+                        }
+                    } else if (is_a) {
                         if (MODE == kGroupedForward) {
                             tc::tma_3d_pair(As, &amap, s * 64, f, tl.e, bar);
                         } else {
                             tc::tma_3d_pair(As, &amap, f, s * 64, tl.e, bar);
                             tc::tma_3d_pair(As + kPanel, &amap, f + 64, s * 64, tl.e, bar);
                         }
+                    } else {
                         if (nbox == 0) tc::tma_2d_pair(Bs, &bmap, s * 64, brow, bar);
                         else
-                            for (int i = 0; i < nbox; ++i)
-                                tc::tma_2d_pair(Bs + i * 32 * 128, &cmap, s * 64, brow + i * 32, bar);
+                            for (int x = 0; x < nbox; ++x)
+                                tc::tma_2d_pair(Bs + x * 32 * 128, &cmap, s * 64, brow + x * 32, bar);
                     }
                 }
                 __syncwarp();
@@ -395,12 +395,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             for (int i = 0; i < nz; ++i) *reinterpret_cast<uint4*>(base + i * 128) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&full_bar[st], 0));
+            if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&full_bar[st], 0), 2);  // for both loaders
         }
     } else if (warp >= 4) {
         // ======================= epilogue: lane = feature, register = column
         const int q = warp & 3;
-        uint8_t* stg = smem + kGroupedStages * kGroupedStage + q * (WG ? 2 : 1) * kEpiWarpBytes;
+        uint8_t* stg = smem + kGroupedStages * kGroupedStage + q * kEpiWarpBytes;
         const bool one = tc::elect_one();
         bool ok = true;
         int it = 0;
@@ -516,52 +516,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         }
                     }
                 } else {
-                    // 32 features x 128 bytes at a time, through two swizzled buffers and tile stores (which
+                    // 32 features x 64 bytes at a time, through two swizzled buffers and tile stores (which
                     // clip at the matrix's edges).  Later parts, and MOE_ACCUMULATE, are added in L2 by the
                     // store itself, each part once the one before has landed: a fixed order of additions
-                    constexpr int kCols = OUT32 ? 32 : 64;
+                    constexpr int kCols = OUT32 ? 16 : 32;
                     if (part > 0) {
                         if (one) tc::store_wait_done();
                         __syncwarp();
                     }
                     if (f < g.F) {
+                        uint32_t r[kCols];
+                        auto load = [&](int c0) {
+#pragma unroll
+                            for (int h = 0; h < kCols; h += 16)
+                                tc::ld16_nowait(tb + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&r[h]));
+                        };
+                        if (!empty) load(0);
                         for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
-                            uint32_t r[32];
-                            uint8_t* buf = stg + ((c0 / kCols) & 1) * kEpiWarpBytes;
-                            if (!empty) {
-                                tc::ld16_nowait(tb + c0, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-                                tc::ld16_nowait(tb + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
-                            }
+                            uint8_t* buf = stg + ((c0 / kCols) & 1) * 2048;
                             if (one) tc::store_wait_read<1>();
+                            if (!empty) tc::ld_wait();
                             __syncwarp();
 #pragma unroll
-                            for (int h = 0; h < kCols; h += 32) {
+                            for (int p = 0; p < 4; ++p) {  // 16-byte pieces of the lane's row
+                                uint4 v = make_uint4(0, 0, 0, 0);
                                 if (!empty) {
-                                    if (h) {
-                                        tc::ld16_nowait(tb + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-                                        tc::ld16_nowait(tb + c0 + h + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
-                                    }
-                                    tc::ld_wait();
-                                }
+                                    if (OUT32) {
+                                        v = make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
+                                    } else {
+                                        uint32_t w[4];
 #pragma unroll
-                                for (int p = 0; p < (OUT32 ? 8 : 4); ++p) {
-                                    uint4 v = make_uint4(0, 0, 0, 0);
-                                    if (!empty) {
-                                        if (OUT32) {
-                                            v = make_uint4(r[4 * p], r[4 * p + 1], r[4 * p + 2], r[4 * p + 3]);
-                                        } else {
-                                            uint32_t w[4];
-#pragma unroll
-                                            for (int i = 0; i < 4; ++i)
-                                                w[i] = pack16(__uint_as_float(r[(8 * p + 2 * i) & 31]),
-                                                              __uint_as_float(r[(8 * p + 2 * i + 1) & 31]), bf16);
-                                            v = make_uint4(w[0], w[1], w[2], w[3]);
-                                        }
+                                        for (int i = 0; i < 4; ++i)
+                                            w[i] = pack16(__uint_as_float(r[(8 * p + 2 * i) % kCols]),
+                                                          __uint_as_float(r[(8 * p + 2 * i + 1) % kCols]), bf16);
+                                        v = make_uint4(w[0], w[1], w[2], w[3]);
                                     }
-                                    const int piece = h / 8 + p;
-                                    *reinterpret_cast<uint4*>(buf + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
                                 }
+                                *reinterpret_cast<uint4*>(buf + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4)) = v;
                             }
+                            if (!empty && c0 + kCols < 256) load(c0 + kCols);  // in flight while this block leaves
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (one) {
@@ -569,8 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                                 else tc::store_3d(&cmap, tl.g0 + c0, f, tl.e, buf);
                                 tc::store_commit();
                             }
-                            __syncwarp();
                         }
+                        if (!empty) tc::ld_wait();
                     }
                 }
                 if (!empty) {
@@ -604,13 +597,13 @@ static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t r
                           int box_rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, str[1] = {(cuuint64_t)ld * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    return encode_sw128(m, elem16(bf16), base, 2, dims, str, box);
+    return encode_tiles(m, elem16(bf16), base, 2, dims, str, box, 128);
 }
 
 template <int MODE, bool OUT32>
 static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
     auto kern = grouped_kernel<MODE, OUT32, false>;
-    constexpr int smem = grouped_smem(MODE);
+    constexpr int smem = kGroupedSmem;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
@@ -624,7 +617,7 @@ static cudaError_t product_maps(GroupedMaps* m, bool forward, bool bf, int E, in
     const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
     const cuuint64_t str[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
     const cuuint32_t box[3] = {64, forward ? 128u : 64u, 1};
-    cudaError_t e = encode_sw128(&m->a, elem16(bf), w, 3, dims, str, box);
+    cudaError_t e = encode_tiles(&m->a, elem16(bf), w, 3, dims, str, box, 128);
     if (e == cudaSuccess) e = map_2d(&m->b, bf, rows, M, forward ? K : N, ld, 128);
     if (e == cudaSuccess) e = map_2d(&m->c, bf, rows, M, forward ? K : N, ld, 32);
     return e;
@@ -646,7 +639,7 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     g.accumulate = p.accumulate;
     g.status = p.status;
     auto kern = grouped_kernel<kGroupedForward, OUT32, true>;
-    constexpr int smem = grouped_smem(kGroupedForward);
+    constexpr int smem = kGroupedSmem;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256);
@@ -679,8 +672,8 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const 
         const int bytes = out_fp32 ? 4 : 2;
         const cuuint64_t dims[3] = {(cuuint64_t)g.C, (cuuint64_t)g.F, (cuuint64_t)g.E};
         const cuuint64_t str[2] = {(cuuint64_t)g.C * bytes, (cuuint64_t)g.F * g.C * bytes};
-        const cuuint32_t box[3] = {(cuuint32_t)(128 / bytes), 32, 1};
-        if (e == cudaSuccess) e = encode_sw128(&m.c, out_fp32 ? Elem::kFp32 : elem16(bf), g.out, 3, dims, str, box);
+        const cuuint32_t box[3] = {(cuuint32_t)(64 / bytes), 32, 1};
+        if (e == cudaSuccess) e = encode_tiles(&m.c, out_fp32 ? Elem::kFp32 : elem16(bf), g.out, 3, dims, str, box, 64);
         if (e != cudaSuccess) return e;
         const int64_t tiles = (int64_t)g.E * JT * ((g.C + 255) / 256);
         return out_fp32 ? grouped_launch<kGroupedWeights, true>(g, m, tiles, s)

@@ -158,11 +158,11 @@ cudaError_t launch_gemm_down(const ExpertArgs& a, const GemmMaps& maps, const fl
                              const int4* desc, const int32_t* counts, cudaStream_t s);
 cudaError_t launch_combine_f16(const CombineArgs& a, const void* o, cudaStream_t s);
 cudaError_t launch_rms_normalize(const void* x, int T, int d, void* out, float eps, cudaStream_t s);
-// a tensor map of a row-major tensor (rank 2 or 3) of bf16, fp16 or fp32, 128-byte swizzle, values outside read as
-// zeros and are not written
+// a tensor map of a row-major tensor (rank 2 or 3) of bf16, fp16 or fp32, 64- or 128-byte swizzle; values outside
+// read as zeros and are not written
 enum class Elem { kBf16, kFp16, kFp32 };
-cudaError_t encode_sw128(CUtensorMap* map, Elem type, const void* base, int rank, const cuuint64_t* dims,
-                         const cuuint64_t* strides_bytes, const cuuint32_t* box);
+cudaError_t encode_tiles(CUtensorMap* map, Elem type, const void* base, int rank, const cuuint64_t* dims,
+                         const cuuint64_t* strides_bytes, const cuuint32_t* box, int swizzle_bytes);
 cudaError_t launch_dequant(const uint8_t* codes, const uint16_t* scales, int N, int K, int bits, float* out,
                            cudaStream_t s);
 

@@ -141,8 +141,8 @@ MOE_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // arrivals on a barrier of any CTA of the cluster (address from cluster_addr)
-MOE_DEV void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+MOE_DEV void arrive_cluster(uint32_t bar, uint32_t count = 1) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 // (relaxed: announces a copy's bytes, publishes no memory of this thread; a
 // release here drains the thread's outstanding operations, ~0.7 us per step)
@@ -221,6 +221,13 @@ MOE_DEV void tma_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z,
         : "memory");
 }
 
+// fetch a tile into L2
+MOE_DEV void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 // TMA tile stores from this CTA's shared memory (bulk groups of the issuing thread)
 MOE_DEV void store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(

@@ -83,9 +83,8 @@ struct GroupedTile {
 
 // The tile list.  Forward and rows products cut a group into blocks of equal
 // size (at most 256 rows, multiples of 32, so that no block is a sliver) and
-// enumerate (group, block, features), features innermost: the CTAs that run
-// together share a group's rows and its matrix through L2.  The weight gradient
-// enumerates (group, k columns, features).
+// enumerate (group, band of blocks, features, block); the weight gradient, with
+// 256-wide k columns in the blocks' place, the same.
 struct TileList {
     const int* start;  // [E + 1] first row of each group
     const int* pre;    // [E + 1] forward, rows: blocks of the groups before this place
@@ -98,21 +97,31 @@ MOE_DEV int block_rows(int c) {
     return blocks <= 1 ? c : (((c + blocks - 1) / blocks) + 31) & ~31;
 }
 
+// Tile t of a group's JT x blocks tiles: bands of 8 blocks, features outside,
+// blocks inside.  The tiles in flight then form a square of the product, whose
+// two operands L2 holds, whatever the number of features.
+MOE_DEV void band(int t, int JT, int blocks, int& jt, int& block) {
+    const int b = t / (8 * JT), in = t - b * 8 * JT, height = min(8, blocks - 8 * b);
+    jt = in / height;
+    block = 8 * b + in - jt * height;
+}
+
 template <int MODE>
 MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const TileList& l, int JT) {
     GroupedTile r;
     if (MODE == kGroupedWeights) {
-        const int per = JT * ((g.C + 255) >> 8);
-        const int place = t / per, in = t - place * per;
+        const int KT = (g.C + 255) >> 8, per = JT * KT;
+        const int place = t / per;
+        int jt, kt;
+        band(t - place * per, JT, KT, jt, kt);
         r.e = l.order[place];
-        r.f0 = (in % JT) << 8;
-        r.g0 = (in / JT) << 8;
+        r.f0 = jt << 8;
+        r.g0 = kt << 8;
         r.row0 = l.start[r.e];
         r.n = l.start[r.e + 1] - r.row0;
         return r;
     }
     const int q = t / JT;
-    r.f0 = (t - q * JT) << 8;
     r.g0 = 0;
     int lo = 0, hi = g.E - 1;  // last place with pre <= q
     while (lo < hi) {
@@ -120,8 +129,12 @@ MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const TileList& l, int 
         if (l.pre[mid] <= q) lo = mid;
         else hi = mid - 1;
     }
+    int jt, at;
+    band(t - l.pre[lo] * JT, JT, l.pre[lo + 1] - l.pre[lo], jt, at);
+    r.f0 = jt << 8;
     r.e = l.order[lo];
-    const int c = l.start[r.e + 1] - l.start[r.e], rows = block_rows(c), at = (q - l.pre[lo]) * rows;
+    const int c = l.start[r.e + 1] - l.start[r.e], rows = block_rows(c);
+    at *= rows;
     r.row0 = l.start[r.e] + at;
     r.n = min(rows, c - at);
     return r;
@@ -343,12 +356,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 for (int s = 0; s < KS; ++s) {
                     const int ps = OUT32 ? s % kPartSteps : s;
                     if (ps == 0 && it > 1) {  // a new part: the next accumulator, once the epilogue has drained it
-                        ok = tc::bar_wait_cluster(&acce_bar[it & 1], ((it >> 1) - 1) & 1, g.status);
+                        ok = tc::bar_wait(&acce_bar[it & 1], ((it >> 1) - 1) & 1, g.status);
                         if (!ok) break;
                     }
-                    // (a cleared step is released by a thread of the other CTA, any other by copies alone)
-                    if (WG && s == KS - 1 && (tl.n & 15)) ok = tc::bar_wait_cluster(&full_bar[st], phase, g.status);
-                    else ok = tc::bar_wait(&full_bar[st], phase, g.status);
+                    ok = tc::bar_wait(&full_bar[st], phase, g.status);
                     if (!ok) break;
                     tc::fence_after();
                     const uint32_t acc = tmem + (it & 1) * 256;

@@ -150,22 +150,6 @@ MOE_DEV void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-// bar_wait for a barrier that other CTAs of the cluster arrive on
-MOE_DEV bool bar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status) {
-    const uint32_t a = smem_addr(bar);
-    for (uint32_t it = 0; it < kSpin; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(a), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    }
-    flag_status(status, kStatusTimeout);
-    return false;
-}
 // One lane of a converged warp, the same at every call.  The branch that this
 // predicate guards keeps its operands in uniform registers, which the issue of
 // MMAs and tensor copies reads; under `lane == 0` each operand is moved there

@@ -139,7 +139,7 @@ def lib() -> ctypes.CDLL:
             L.moe_swiglu_backward.restype = st
             L.moe_swiglu_backward.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp, u32, vp]
             L.moe_adapter_workspace.restype = ctypes.c_size_t
-            L.moe_adapter_workspace.argtypes = [i32, i32, i32]
+            L.moe_adapter_workspace.argtypes = [i32, i32]
             L.moe_adapter_project.restype = st
             L.moe_adapter_project.argtypes = [ctypes.POINTER(MoeAdapterArgs), u32, vp]
             L.moe_check_op_status.restype = st

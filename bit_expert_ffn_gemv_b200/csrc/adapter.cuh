@@ -1,17 +1,36 @@
-// adapter.cuh -- the delta B_a v_t of 16 tokens by a warp's 32 features, as
-// warp-MMA fragments.
+// adapter.cuh -- the inner values v of the tokens' adapters and their delta
+// B_a v_t, as warp-MMA fragments of 32 features by 16 tokens.
 //
 // v is fp32; the MMA takes 16-bit operands, so v is split into terms of B's
 // type (v = hi + lo [+ lower], each exact in what the ones before leave): two
 // terms hold 16 bits of v in bf16 and 22 in fp16, three hold 24 in bf16, which
 // fp32 results use.  fp16's range is too small for v: each token's values are
-// first scaled by a power of two that brings the largest to [1, 2).
+// first scaled by a power of two that brings the largest into [1, 2), undone
+// in the result.  The split is made once, where v is computed.
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
 #include "pack16.cuh"
 
 namespace moe {
+
+// Split v, per token r / 4 quads of four rank values: 16 bytes {hi01, hi23,
+// lo01, lo23}, and with three terms 16 more {lower01, lower23, -, -}; then
+// (fp16) one factor per token.  fp32 v: [token][r].
+MOE_DEV int quad_vectors(int terms) { return terms == 3 ? 2 : 1; }
+MOE_DEV float* adapter_back(const AdapterArgs& p, int terms) {
+    return reinterpret_cast<float*>(static_cast<uint4*>(p.v) + (int64_t)p.T * (p.r >> 2) * quad_vectors(terms));
+}
+
+// the next term of two values: packed, and what it leaves (an infinite term leaves nothing)
+template <bool BF16>
+MOE_DEV uint32_t take_term(float& a, float& b) {
+    const uint32_t t = pack2<BF16>(a, b);
+    const float2 x = unpack2<BF16>(t);
+    a = isinf(x.x) ? 0.f : a - x.x;
+    b = isinf(x.y) ? 0.f : b - x.y;
+    return t;
+}
 
 // d[m][n][i]: feature 16 m + lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2
 struct DeltaFrags {
@@ -20,24 +39,10 @@ struct DeltaFrags {
 MOE_DEV int frag_feature(int m, int i) { return 16 * m + ((threadIdx.x & 31) >> 2) + 8 * (i >> 1); }
 MOE_DEV int frag_token(int n, int i) { return 8 * n + 2 * (threadIdx.x & 3) + (i & 1); }
 
-// The lane's four v values of rank j..j+3 of token t, summed over the slices.
-MOE_DEV float4 adapter_v(const AdapterArgs& p, int t, int j) {
-    const float* q = p.v + (int64_t)t * p.r + j;
-    float4 s = *reinterpret_cast<const float4*>(q);
-    for (int i = 1; i < p.slices; ++i) {
-        const float4 u = *reinterpret_cast<const float4*>(q + (int64_t)i * p.T * p.r);
-        s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
-    }
-    return s;
-}
-
-template <bool BF16>
-MOE_DEV float next_term(float v, float term) {  // what the term leaves (an infinite term leaves nothing)
-    return isinf(term) ? 0.f : v - term;
-}
-
 // Frags of B_a[f0 .. f0 + 31] . v of tokens t0 .. t0 + 15 that are in `used`
-// (a bit per token; the others' columns hold nothing meaningful).
+// (a bit per token; the others' columns hold nothing meaningful).  Lane l / 4
+// reads token l / 4 (+ 8) and feature rows l / 4 + 8 i; lane l % 4 takes four
+// consecutive rank values of each, the same for both operands.
 template <bool BF16, int TERMS>
 MOE_DEV void adapter_delta(const AdapterArgs& p, int t0, uint32_t used, int a, int f0, DeltaFrags& out) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
@@ -51,59 +56,45 @@ MOE_DEV void adapter_delta(const AdapterArgs& p, int t0, uint32_t used, int a, i
     const uint16_t* row[4];  // features f0 + gq + 8 i (past N: any row, its results are not stored)
 #pragma unroll
     for (int i = 0; i < 4; ++i) row[i] = B + (int64_t)min(f0 + gq + 8 * i, p.N - 1) * p.r;
-    float back[2] = {1.f, 1.f};  // fp16: undoes the scale of token 8 n + gq
-    float scale[2] = {1.f, 1.f};
-    if (!BF16) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float most = 0.f;
-            if ((used >> (8 * n + gq)) & 1)
-                for (int j = 4 * c; j < p.r; j += 16) {
-                    const float4 v = adapter_v(p, t0 + 8 * n + gq, j);
-                    most = fmaxf(fmaxf(fmaxf(most, fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
-                }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);  // biased exponent
-            scale[n] = __uint_as_float((uint32_t)(254 - e) << 23);
-            back[n] = __uint_as_float((uint32_t)e << 23);
-        }
-    }
-#pragma unroll 2
-    for (int j0 = 0; j0 < p.r; j0 += 16) {
-        const int j = j0 + 4 * c;
+    constexpr int kVecs = TERMS == 3 ? 2 : 1;
+    const int quads = p.r >> 2;
+    const uint4* v0 = static_cast<const uint4*>(p.v) + (int64_t)(t0 + gq) * quads * kVecs;
+    const bool use[2] = {((used >> gq) & 1) != 0, ((used >> (8 + gq)) & 1) != 0};
+#pragma unroll 4
+    for (int q0 = 0; q0 < quads; q0 += 4) {
+        const int q = q0 + c;
         uint2 w[4];
-        float4 v[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = j < p.r ? __ldg(reinterpret_cast<const uint2*>(row[i] + j)) : make_uint2(0, 0);
+        for (int i = 0; i < 4; ++i) w[i] = q < quads ? __ldg(reinterpret_cast<const uint2*>(row[i] + 4 * q)) : make_uint2(0, 0);
+        uint4 v[2][kVecs];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            v[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j < p.r && ((used >> (8 * n + gq)) & 1)) v[n] = adapter_v(p, t0 + 8 * n + gq, j);
-            if (!BF16) v[n].x *= scale[n], v[n].y *= scale[n], v[n].z *= scale[n], v[n].w *= scale[n];
-        }
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                v[n][k] = make_uint4(0, 0, 0, 0);
+                if (q < quads && use[n]) v[n][k] = v0[((int64_t)n * 8 * quads + q) * kVecs + k];
+            }
         const uint32_t f0r[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, f1r[4] = {w[2].x, w[3].x, w[2].y, w[3].y};
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int term = 0; term < TERMS; ++term) {
-                const uint32_t b0 = pack2<BF16>(v[n].x, v[n].y), b1 = pack2<BF16>(v[n].z, v[n].w);
-                mma16<BF16>(out.d[0][n], f0r, b0, b1);
-                mma16<BF16>(out.d[1][n], f1r, b0, b1);
-                if (term + 1 < TERMS) {
-                    const float2 x0 = unpack2<BF16>(b0), x1 = unpack2<BF16>(b1);
-                    v[n] = make_float4(next_term<BF16>(v[n].x, x0.x), next_term<BF16>(v[n].y, x0.y),
-                                       next_term<BF16>(v[n].z, x1.x), next_term<BF16>(v[n].w, x1.y));
-                }
+            mma16<BF16>(out.d[0][n], f0r, v[n][0].x, v[n][0].y);
+            mma16<BF16>(out.d[1][n], f1r, v[n][0].x, v[n][0].y);
+            mma16<BF16>(out.d[0][n], f0r, v[n][0].z, v[n][0].w);
+            mma16<BF16>(out.d[1][n], f1r, v[n][0].z, v[n][0].w);
+            if (TERMS == 3) {
+                mma16<BF16>(out.d[0][n], f0r, v[n][kVecs - 1].x, v[n][kVecs - 1].y);
+                mma16<BF16>(out.d[1][n], f1r, v[n][kVecs - 1].x, v[n][kVecs - 1].y);
             }
         }
     }
     if (!BF16) {
+        const float* back = adapter_back(p, TERMS) + t0;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float s = __shfl_sync(0xffffffffu, back[n], (2 * c + i) * 4);
+                const int t = 8 * n + 2 * c + i;
+                const float s = (used >> t) & 1 ? back[t] : 1.f;
                 out.d[0][n][i] *= s, out.d[0][n][i + 2] *= s, out.d[1][n][i] *= s, out.d[1][n][i + 2] *= s;
             }
     }

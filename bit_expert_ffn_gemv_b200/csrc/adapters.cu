@@ -17,50 +17,57 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "pack16.cuh"
+#include "tc.cuh"
 
 namespace moe {
 
 // ---------------------------------------------------------------- shrink
-// One CTA: a window of WIN tokens, one slice of K.  The window's tokens are
-// grouped by adapter with one match instruction, in any order of ids, and cut
-// into items of up to eight tokens of one adapter, whose A rows are read once:
-// MMAs of 16 A rows by 8 tokens, both operands loaded 16 bytes a lane in the
-// same permuted order of k.  The eight warps take an item each; with fewer
-// items several warps share one and split its K.  Bound by the A rows of a
-// decode batch (every token another adapter) or the x of a prefill chunk.
+// A cluster of CTAs owns a window of WIN tokens and splits K; its CTAs' sums
+// meet through distributed shared memory in rank order, so v is written once,
+// already scaled, in the form its reader takes (adapter.cuh).  Inside a CTA the
+// window's tokens are grouped by adapter with one match instruction, in any
+// order of ids, into items of up to WIN tokens of one adapter, whose A rows
+// are read once: MMAs of 16 A rows by 8 tokens, both operands loaded 16 bytes a
+// lane in the same permuted order of k.  The eight warps take an item each;
+// with fewer items several warps share one and split its K.  Bound by the A
+// rows of a decode batch (every token another adapter) or the x of a prefill
+// chunk.
 constexpr int kShrinkThreads = 256;
-constexpr int kShrinkRows = 64;  // A rows per pass
 
-template <bool BF16, int WIN>
+// rank values per pass and octets of tokens per item: the accumulators stay in registers
+template <int WIN>
+struct ShrinkCfg {
+    static constexpr int kOctets = WIN / 8, kRows = WIN == 8 ? 64 : 32, kTiles = kRows / 16, kPitch = kRows + 4;
+    static constexpr int kRed = 8 * WIN * kPitch * 4;  // bytes: [warp][token of its item][row]
+};
+
+template <bool BF16, int WIN, int TERMS>
 __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArgs p) {
-    __shared__ float red[8][8][kShrinkRows + 4];  // [warp][token of its item][row]
-    __shared__ int item_adapter[WIN], item_tok[WIN][8];
+    using C = ShrinkCfg<WIN>;
+    extern __shared__ __align__(16) uint8_t shrink_smem[];
+    float* red = reinterpret_cast<float*>(shrink_smem);                 // [8][WIN][kPitch]
+    float* sums = reinterpret_cast<float*>(shrink_smem + C::kRed);      // [WIN][r]
+    __shared__ int item_adapter[WIN], item_count[WIN];
+    __shared__ int8_t item_tok[WIN][WIN];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, c = lane & 3;
     const int t0 = blockIdx.x * WIN, slice = blockIdx.y;
-    const int per = ((p.K + p.slices - 1) / p.slices + 31) & ~31;  // K of a slice
+    const int per = ((p.K + p.slices - 1) / p.slices + 31) & ~31;  // K of a CTA
     const int sb = slice * per, se = min(p.K, sb + per);
     const int t = t0 + lane;
     int id = lane < WIN && t < p.T ? __ldg(&p.ids[t]) : -1;
     if (id < 0 || id >= p.L) id = -1;
     const uint32_t mine = __match_any_sync(0xffffffffu, id);
-    // this lane's token is number `order` of its group; every eighth begins an item
-    const int order = __popc(mine & ((1u << lane) - 1));
-    const bool begins = id >= 0 && (order & 7) == 0;
+    const bool begins = id >= 0 && (mine & ((1u << lane) - 1)) == 0;  // the adapter's first token
     const uint32_t starts = __ballot_sync(0xffffffffu, begins);
     const int items = __popc(starts);
-    if (items == 0) return;
-    if (warp == 0) {
-        if (begins) {
-            const int it = __popc(starts & ((1u << lane) - 1));
-            item_adapter[it] = id;
-            uint32_t rest = mine & ~((1u << lane) - 1);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                item_tok[it][i] = rest ? __ffs(rest) - 1 : -1;
-                rest &= rest - 1;
-            }
-        }
+    if (items == 0) return;  // (the whole cluster)
+    if (warp == 0 && begins) {
+        const int it = __popc(starts & ((1u << lane) - 1));
+        item_adapter[it] = id;
+        int n = 0;
+        for (uint32_t rest = mine; rest; rest &= rest - 1) item_tok[it][n++] = (int8_t)(__ffs(rest) - 1);
+        item_count[it] = n;
     }
     __syncthreads();
     const int share = items == 1 ? 8 : items == 2 ? 4 : items <= 4 ? 2 : 1;  // warps per item
@@ -71,57 +78,136 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArg
     const uint16_t* A = static_cast<const uint16_t*>(p.a);
     for (int base = 0; base < items; base += at_once) {
         const int it = base + warp / share;
-        const bool live = it < items;
-        const int a = live ? item_adapter[it] : 0, tok = live ? item_tok[it][gq] : -1;
-        const uint16_t* xr = x + (int64_t)(t0 + (tok < 0 ? 0 : tok)) * p.ldx;
-        for (int j0 = 0; j0 < p.r; j0 += kShrinkRows) {
-            const int rows = min(kShrinkRows, p.r - j0), tiles = (rows + 15) >> 4;
-            float acc[4][4] = {};
+        const int n = it < items ? item_count[it] : 0, a = n ? item_adapter[it] : 0;
+        const int octets = (n + 7) >> 3;
+        const uint16_t* xr[C::kOctets];
+#pragma unroll
+        for (int o = 0; o < C::kOctets; ++o)
+            xr[o] = x + (int64_t)(t0 + (8 * o + gq < n ? item_tok[it][8 * o + gq] : 0)) * p.ldx;
+        for (int j0 = 0; j0 < p.r; j0 += C::kRows) {
+            const int rows = min(C::kRows, p.r - j0), tiles = (rows + 15) >> 4;
+            float acc[C::kTiles][C::kOctets][4] = {};
             const uint16_t* ar = A + ((int64_t)a * p.r + j0) * p.K;
-            if (live) {
-#pragma unroll 4
+            if (n) {
+#pragma unroll 2
                 for (int k0 = kb; k0 < ke; k0 += 32) {
                     const int k = k0 + 8 * c;
                     const bool in = k < ke;
-                    uint4 bv = make_uint4(0, 0, 0, 0);
-                    if (in && tok >= 0) bv = __ldg(reinterpret_cast<const uint4*>(xr + k));
+                    uint4 bv[C::kOctets];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int o = 0; o < C::kOctets; ++o) {
+                        bv[o] = make_uint4(0, 0, 0, 0);
+                        if (in && 8 * o + gq < n) bv[o] = __ldg(reinterpret_cast<const uint4*>(xr[o] + k));
+                    }
+#pragma unroll
+                    for (int q = 0; q < C::kTiles; ++q) {
                         if (q >= tiles) break;
                         const int r0 = q * 16 + gq;
                         uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
                         if (in && r0 < rows) lo = __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)r0 * p.K + k));
                         if (in && r0 + 8 < rows) hi = __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)(r0 + 8) * p.K + k));
                         const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
-                        mma16<BF16>(acc[q], f0, bv.x, bv.y);
-                        mma16<BF16>(acc[q], f1, bv.z, bv.w);
+#pragma unroll
+                        for (int o = 0; o < C::kOctets; ++o) {
+                            if (o >= octets) break;
+                            mma16<BF16>(acc[q][o], f0, bv[o].x, bv[o].y);
+                            mma16<BF16>(acc[q][o], f1, bv[o].z, bv[o].w);
+                        }
                     }
                 }
             }
             __syncthreads();  // the last pass's sums have been read
+            float* mr = red + warp * WIN * C::kPitch;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (q >= tiles) break;
-                red[warp][2 * c][q * 16 + gq] = acc[q][0];
-                red[warp][2 * c + 1][q * 16 + gq] = acc[q][1];
-                red[warp][2 * c][q * 16 + gq + 8] = acc[q][2];
-                red[warp][2 * c + 1][q * 16 + gq + 8] = acc[q][3];
-            }
+            for (int q = 0; q < C::kTiles; ++q)
+#pragma unroll
+                for (int o = 0; o < C::kOctets; ++o) {
+                    if (q >= tiles || o >= octets) break;
+                    float* m = mr + (8 * o + 2 * c) * C::kPitch + q * 16 + gq;
+                    m[0] = acc[q][o][0];
+                    m[C::kPitch] = acc[q][o][1];
+                    m[8] = acc[q][o][2];
+                    m[C::kPitch + 8] = acc[q][o][3];
+                }
             __syncthreads();
-            // each warp writes one token of each of the items in turn, the shares added in order
-            for (int i = warp; i < at_once * 8; i += 8) {
-                const int w = (i >> 3) * share, m = i & 7, ii = base + (i >> 3);
-                const int at = ii < items ? item_tok[ii][m] : -1;
-                if (at < 0) continue;
-                const float sc = p.scale ? __ldg(&p.scale[item_adapter[ii]]) : 1.0f;
+            // the shares of each item, added in order
+            for (int i = warp; i < at_once * WIN; i += 8) {
+                const int slot = i / WIN, m = i % WIN, ii = base + slot;
+                if (ii >= items || m >= item_count[ii]) continue;
+                const float* src = red + (slot * share * WIN + m) * C::kPitch;
+                float* dst = sums + item_tok[ii][m] * p.r + j0;
                 for (int j = lane; j < rows; j += 32) {
-                    float s = red[w][m][j];
-                    for (int q = 1; q < share; ++q) s += red[w + q][m][j];
-                    p.v[((int64_t)slice * p.T + t0 + at) * p.r + j0 + j] = sc * s;
+                    float s = src[j];
+                    for (int q = 1; q < share; ++q) s += src[q * WIN * C::kPitch + j];
+                    dst[j] = s;
                 }
             }
         }
     }
+    if (p.slices > 1) tc::cluster_sync();
+    else __syncthreads();
+    // each CTA finishes its share of the tokens, a warp a token
+    const int quads = p.r >> 2;
+    for (int m = slice * 8 + warp; m < WIN; m += 8 * p.slices) {
+        const int a = __shfl_sync(0xffffffffu, id, m);
+        if (a < 0) continue;
+        const float sc = p.scale ? __ldg(&p.scale[a]) : 1.0f;
+        float4 v[2];  // quads lane, lane + 32 (rank <= 256)
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int q = lane + 32 * i;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q < quads) {
+                const float* at = sums + m * p.r + 4 * q;
+                if (p.slices == 1) {
+                    v[i] = *reinterpret_cast<const float4*>(at);
+                } else {
+                    for (int s = 0; s < p.slices; ++s) {
+                        const float4 u = tc::ld_cluster4(tc::cluster_addr(at, s));
+                        v[i].x += u.x, v[i].y += u.y, v[i].z += u.z, v[i].w += u.w;
+                    }
+                }
+                v[i].x *= sc, v[i].y *= sc, v[i].z *= sc, v[i].w *= sc;
+            }
+            most = fmaxf(fmaxf(fmaxf(most, fabsf(v[i].x)), fmaxf(fabsf(v[i].y), fabsf(v[i].z))), fabsf(v[i].w));
+        }
+        if (TERMS == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (lane + 32 * i < quads)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.v) + (int64_t)(t0 + m) * p.r + 4 * (lane + 32 * i)) = v[i];
+            continue;
+        }
+        float scale = 1.f;
+        if (!BF16) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);  // biased exponent
+            scale = __uint_as_float((uint32_t)(254 - e) << 23);
+            if (lane == 0) adapter_back(p, TERMS)[t0 + m] = __uint_as_float((uint32_t)e << 23);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int q = lane + 32 * i;
+            if (q >= quads) continue;
+            float4 u = v[i];
+            if (!BF16) u.x *= scale, u.y *= scale, u.z *= scale, u.w *= scale;
+            uint4 o;
+            o.x = take_term<BF16>(u.x, u.y);
+            o.y = take_term<BF16>(u.z, u.w);
+            o.z = take_term<BF16>(u.x, u.y);
+            o.w = take_term<BF16>(u.z, u.w);
+            uint4* dst = static_cast<uint4*>(p.v) + ((int64_t)(t0 + m) * quads + q) * (TERMS == 3 ? 2 : 1);
+            dst[0] = o;
+            if (TERMS == 3) {
+                o.x = take_term<BF16>(u.x, u.y);
+                o.y = take_term<BF16>(u.z, u.w);
+                dst[1] = make_uint4(o.x, o.y, 0, 0);
+            }
+        }
+    }
+    if (p.slices > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------- the delta alone
@@ -168,24 +254,53 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
 // tokens of different adapters, and more windows share its A rows out.
 constexpr int kSmallWindowTokens = 256;
 
-int adapter_slices(int T, int K) {
-    // slices of K: CTAs for every SM as long as a slice keeps 256 of K
-    const int win = T <= kSmallWindowTokens ? 8 : 32;
-    const int windows = (T + win - 1) / win, most = (K + 255) / 256;
-    const int want = (148 + windows - 1) / windows;
-    return want < most ? want : most;
+// CTAs that split a window's K: a power of two up to 8, so that the windows'
+// CTAs fill the GPU once while each keeps at least 256 of K.
+static int shrink_slices(int T, int K) {
+    const int win = T <= kSmallWindowTokens ? 8 : 32, windows = (T + win - 1) / win;
+    int s = 1;
+    while (s < 8 && windows * s < 148 && 2 * s * 256 <= K) s *= 2;
+    return s;
 }
 
-template <bool BF16>
-static cudaError_t adapters(const AdapterArgs& p, bool out32, cudaStream_t s) {
-    if (p.T <= kSmallWindowTokens)
-        shrink_kernel<BF16, 8><<<dim3((p.T + 7) / 8, p.slices), kShrinkThreads, 0, s>>>(p);
-    else
-        shrink_kernel<BF16, 32><<<dim3((p.T + 31) / 32, p.slices), kShrinkThreads, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+size_t adapter_workspace(int T, int r) {
+    // the largest form: two 16-byte vectors per four rank values, and a factor per token
+    return (size_t)T * (r / 4) * 32 + (((size_t)T * 4 + 15) & ~size_t(15));
+}
+
+template <bool BF16, int WIN, int TERMS>
+static cudaError_t shrink(const AdapterArgs& p, cudaStream_t s) {
+    auto kern = shrink_kernel<BF16, WIN, TERMS>;
+    const int smem = ShrinkCfg<WIN>::kRed + WIN * p.r * 4;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         ShrinkCfg<WIN>::kRed + WIN * kMaxAdapterRank * 4);
     if (e != cudaSuccess) return e;
-    if (p.w) return p.T <= kSkinnyMaxRows ? launch_skinny_adapter(p, BF16, out32, s)
-                                          : launch_grouped_adapter(p, BF16, out32, s);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 1;
+    at.val.clusterDim.y = (unsigned)p.slices;
+    at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((p.T + WIN - 1) / WIN, p.slices);
+    cfg.blockDim = kShrinkThreads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool BF16, bool OUT32>
+static cudaError_t adapters(AdapterArgs p, cudaStream_t s) {
+    constexpr int kTerms = BF16 && OUT32 ? 3 : 2;
+    p.slices = shrink_slices(p.T, p.K);
+    const bool skinny = p.w && p.T <= kSkinnyMaxRows;
+    const cudaError_t e = skinny                        ? shrink<BF16, 8, 0>(p, s)
+                          : p.T <= kSmallWindowTokens ? shrink<BF16, 8, kTerms>(p, s)
+                                                        : shrink<BF16, 32, kTerms>(p, s);
+    if (e != cudaSuccess) return e;
+    if (skinny) return launch_skinny_adapter(p, BF16, OUT32, s);
+    if (p.w) return launch_grouped_adapter(p, BF16, OUT32, s);
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
@@ -195,12 +310,12 @@ static cudaError_t adapters(const AdapterArgs& p, bool out32, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return out32 ? cudaLaunchKernelEx(&cfg, expand_kernel<BF16, true>, p)
-                 : cudaLaunchKernelEx(&cfg, expand_kernel<BF16, false>, p);
+    return cudaLaunchKernelEx(&cfg, expand_kernel<BF16, OUT32>, p);
 }
 
 cudaError_t launch_adapters(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {
-    return bf16 ? adapters<true>(p, out32, s) : adapters<false>(p, out32, s);
+    if (bf16) return out32 ? adapters<true, true>(p, s) : adapters<true, false>(p, s);
+    return out32 ? adapters<false, true>(p, s) : adapters<false, false>(p, s);
 }
 
 }  // namespace moe

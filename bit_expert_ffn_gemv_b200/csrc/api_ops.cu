@@ -18,7 +18,7 @@ namespace {
 constexpr int kMaxGroups = 1024;
 constexpr int32_t kMaxRows = 1 << 27;  // row blocks of all groups and their tiles stay inside 32 bits
 constexpr int32_t kMaxCols = 1 << 17;
-constexpr int32_t kMaxRank = 256;
+constexpr int32_t kMaxRank = moe::kMaxAdapterRank;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool good(const void* p) { return p && aligned16(p); }
@@ -138,9 +138,9 @@ moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int
     return cuda_status(moe::launch_swiglu(a, !(flags & MOE_OP_FP16), true, static_cast<cudaStream_t>(stream)));
 }
 
-size_t moe_adapter_workspace(int32_t tokens, int32_t k, int32_t rank) {
-    if (tokens <= 0 || tokens > kMaxRows || k <= 0 || k > kMaxCols || rank <= 0 || rank > kMaxRank) return 0;
-    return sizeof(float) * (size_t)moe::adapter_slices(tokens, k) * tokens * rank;
+size_t moe_adapter_workspace(int32_t tokens, int32_t rank) {
+    if (tokens <= 0 || tokens > kMaxRows || rank <= 0 || rank > kMaxRank) return 0;
+    return moe::adapter_workspace(tokens, rank);
 }
 
 moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, void* stream) {
@@ -152,7 +152,7 @@ moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, voi
     if (q.tokens == 0) return MOE_OK;
     if (!good(q.x) || !good(q.a) || !good(q.b) || !good(q.y) || !good(q.workspace) || (q.w && !aligned16(q.w)) ||
         !q.ids || (reinterpret_cast<uintptr_t>(q.ids) & 3u) || (reinterpret_cast<uintptr_t>(q.scale) & 3u) ||
-        q.workspace_bytes < moe_adapter_workspace(q.tokens, q.k, q.rank) || q.x == q.y)
+        q.workspace_bytes < moe_adapter_workspace(q.tokens, q.rank) || q.x == q.y)
         return MOE_ERR_INVALID_ARG;
     moe::AdapterArgs a{};
     a.x = q.x;
@@ -169,8 +169,7 @@ moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, voi
     a.ids = q.ids;
     a.y = q.y;
     a.ldy = q.ldy;
-    a.v = static_cast<float*>(q.workspace);
-    a.slices = moe::adapter_slices(q.tokens, q.k);
+    a.v = q.workspace;
     a.accumulate = (flags & MOE_ACCUMULATE) ? 1 : 0;
     if (status_word(&a.status) != cudaSuccess) return MOE_ERR_CUDA;
     return cuda_status(moe::launch_adapters(a, !(flags & MOE_OP_FP16), (flags & MOE_OUT_FP32) != 0,

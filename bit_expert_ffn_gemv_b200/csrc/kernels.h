@@ -217,12 +217,13 @@ struct AdapterArgs {
     const int32_t* ids;  // [T]
     void* y;             // [T x N], pitch ldy
     int64_t ldy;
-    float* v;            // workspace [slices x T x r]: scale * A x, per slice of K
-    int slices;
+    void* v;             // workspace (adapter_workspace): scale * A x of each token
+    int slices;          // CTAs that split K in the first kernel
     int accumulate;
     uint32_t* status;
 };
-int adapter_slices(int T, int K);
+constexpr int kMaxAdapterRank = 256;
+size_t adapter_workspace(int T, int r);
 cudaError_t launch_adapters(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s);
 cudaError_t launch_skinny_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s);
 cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s);

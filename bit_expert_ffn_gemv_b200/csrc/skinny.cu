@@ -154,13 +154,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
             __syncthreads();
             for (int i = tid; i < n * quads; i += kSkinnyThreads) {
                 const int m = i / quads, jq = (i - m * quads) * 4;
-                const float* src = ad.v + (int64_t)m * ad.r + j0 + jq;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int sl = 0; sl < ad.slices; ++sl) {
-                    const float4 u = *reinterpret_cast<const float4*>(src + (int64_t)sl * ad.T * ad.r);
-                    a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
-                }
+                const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(ad.v) + (int64_t)m * ad.r + j0 + jq);
                 *reinterpret_cast<float4*>(v + m * kBlock + jq) = a;
             }
             __syncthreads();

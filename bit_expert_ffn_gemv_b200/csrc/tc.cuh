@@ -140,6 +140,14 @@ MOE_DEV uint32_t cluster_addr(const void* p, uint32_t rank) {
 MOE_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+MOE_DEV float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 // arrivals on a barrier of any CTA of the cluster (address from cluster_addr)
 MOE_DEV void arrive_cluster(uint32_t bar, uint32_t count = 1) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");

@@ -196,7 +196,7 @@ def adapter_project(x, a, b, ids, w=None, scale=None, out=None, flags=0, stream=
     if out is None:
         out = torch.empty((T, n), dtype=dt, device=x.device)
     _matrix(out, "out", x, n, T, (dt,))
-    size = lib().moe_adapter_workspace(T, k, rank)
+    size = lib().moe_adapter_workspace(T, rank)
     ws = torch.empty(size, dtype=torch.uint8, device=x.device)
     if stream is not None:
         ws.record_stream(stream)  # freed below, possibly before the call has run on its stream

@@ -492,7 +492,7 @@ typedef struct {
 } moe_adapter_args;
 
 /* Workspace bytes of moe_adapter_project (0 for arguments out of range). */
-size_t moe_adapter_workspace(int32_t tokens, int32_t k, int32_t rank);
+size_t moe_adapter_workspace(int32_t tokens, int32_t rank);
 
 /*
  * x and y must not overlap.  Errors: INVALID_ARG (a field out of the ranges

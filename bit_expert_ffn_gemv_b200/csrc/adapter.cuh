@@ -4,9 +4,10 @@
 // v is fp32; the MMA takes 16-bit operands, so v is split into terms of B's
 // type (v = hi + lo [+ lower], each exact in what the ones before leave): two
 // terms hold 16 bits of v in bf16 and 22 in fp16, three hold 24 in bf16, which
-// fp32 results use.  fp16's range is too small for v: each token's values are
-// first scaled by a power of two that brings the largest into [1, 2), undone
-// in the result.  The split is made once, where v is computed.
+// fp32 results use.  The split is made once, where v is computed.  fp16's range
+// is too small for v: a token whose largest value lies outside [2^-2, 2^15) is
+// first scaled by a power of two that brings it into [1, 2), undone in the
+// result (inside the range the two terms hold 2^-23 of that largest value).
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
@@ -14,21 +15,21 @@
 
 namespace moe {
 
-// Split v, per token r / 4 quads of four rank values: 16 bytes {hi01, hi23,
-// lo01, lo23}, and with three terms 16 more {lower01, lower23, -, -}; then
-// (fp16) one factor per token.  fp32 v: [token][r].
-MOE_DEV int quad_vectors(int terms) { return terms == 3 ? 2 : 1; }
+// Split v: `terms` row-major 16-bit matrices [T x r], then (fp16) the factor
+// that undoes each token's scale.  fp32 v: [T x r].
+MOE_DEV const uint16_t* adapter_term(const AdapterArgs& p, int term) {
+    return static_cast<const uint16_t*>(p.v) + (int64_t)term * p.T * p.r;
+}
 MOE_DEV float* adapter_back(const AdapterArgs& p, int terms) {
-    return reinterpret_cast<float*>(static_cast<uint4*>(p.v) + (int64_t)p.T * (p.r >> 2) * quad_vectors(terms));
+    return reinterpret_cast<float*>(static_cast<uint16_t*>(p.v) + (int64_t)terms * p.T * p.r);
 }
 
-// the next term of two values: packed, and what it leaves (an infinite term leaves nothing)
+// the next term of a value, and what it leaves (an infinite term leaves nothing)
 template <bool BF16>
-MOE_DEV uint32_t take_term(float& a, float& b) {
-    const uint32_t t = pack2<BF16>(a, b);
-    const float2 x = unpack2<BF16>(t);
-    a = isinf(x.x) ? 0.f : a - x.x;
-    b = isinf(x.y) ? 0.f : b - x.y;
+MOE_DEV uint16_t take_term(float& v) {
+    const uint16_t t = pack1<BF16>(v);
+    const float x = unpack1<BF16>(t);
+    v = isinf(x) ? 0.f : v - x;
     return t;
 }
 
@@ -56,36 +57,31 @@ MOE_DEV void adapter_delta(const AdapterArgs& p, int t0, uint32_t used, int a, i
     const uint16_t* row[4];  // features f0 + gq + 8 i (past N: any row, its results are not stored)
 #pragma unroll
     for (int i = 0; i < 4; ++i) row[i] = B + (int64_t)min(f0 + gq + 8 * i, p.N - 1) * p.r;
-    constexpr int kVecs = TERMS == 3 ? 2 : 1;
     const int quads = p.r >> 2;
-    const uint4* v0 = static_cast<const uint4*>(p.v) + (int64_t)(t0 + gq) * quads * kVecs;
     const bool use[2] = {((used >> gq) & 1) != 0, ((used >> (8 + gq)) & 1) != 0};
+    const int64_t vrow = (int64_t)(t0 + gq) * p.r;
 #pragma unroll 4
     for (int q0 = 0; q0 < quads; q0 += 4) {
         const int q = q0 + c;
-        uint2 w[4];
+        uint2 w[4], v[2][TERMS];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = q < quads ? __ldg(reinterpret_cast<const uint2*>(row[i] + 4 * q)) : make_uint2(0, 0);
-        uint4 v[2][kVecs];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                v[n][k] = make_uint4(0, 0, 0, 0);
-                if (q < quads && use[n]) v[n][k] = v0[((int64_t)n * 8 * quads + q) * kVecs + k];
+            for (int k = 0; k < TERMS; ++k) {
+                v[n][k] = make_uint2(0, 0);
+                if (q < quads && use[n])
+                    v[n][k] = *reinterpret_cast<const uint2*>(adapter_term(p, k) + vrow + (int64_t)n * 8 * p.r + 4 * q);
             }
         const uint32_t f0r[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, f1r[4] = {w[2].x, w[3].x, w[2].y, w[3].y};
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            mma16<BF16>(out.d[0][n], f0r, v[n][0].x, v[n][0].y);
-            mma16<BF16>(out.d[1][n], f1r, v[n][0].x, v[n][0].y);
-            mma16<BF16>(out.d[0][n], f0r, v[n][0].z, v[n][0].w);
-            mma16<BF16>(out.d[1][n], f1r, v[n][0].z, v[n][0].w);
-            if (TERMS == 3) {
-                mma16<BF16>(out.d[0][n], f0r, v[n][kVecs - 1].x, v[n][kVecs - 1].y);
-                mma16<BF16>(out.d[1][n], f1r, v[n][kVecs - 1].x, v[n][kVecs - 1].y);
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+                mma16<BF16>(out.d[0][n], f0r, v[n][k].x, v[n][k].y);
+                mma16<BF16>(out.d[1][n], f1r, v[n][k].x, v[n][k].y);
             }
-        }
     }
     if (!BF16) {
         const float* back = adapter_back(p, TERMS) + t0;

@@ -42,7 +42,7 @@ struct ShrinkCfg {
 };
 
 template <bool BF16, int WIN, int TERMS>
-__global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArgs p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const AdapterArgs p) {
     using C = ShrinkCfg<WIN>;
     extern __shared__ __align__(16) uint8_t shrink_smem[];
     float* red = reinterpret_cast<float*>(shrink_smem);                 // [8][WIN][kPitch]
@@ -80,40 +80,56 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArg
         const int it = base + warp / share;
         const int n = it < items ? item_count[it] : 0, a = n ? item_adapter[it] : 0;
         const int octets = (n + 7) >> 3;
+        // (columns and rows past the item's end repeat its first: their sums are not read)
         const uint16_t* xr[C::kOctets];
 #pragma unroll
         for (int o = 0; o < C::kOctets; ++o)
-            xr[o] = x + (int64_t)(t0 + (8 * o + gq < n ? item_tok[it][8 * o + gq] : 0)) * p.ldx;
+            xr[o] = x + (int64_t)(t0 + (8 * o + gq < n ? item_tok[it][8 * o + gq] : n ? item_tok[it][0] : 0)) * p.ldx + 8 * c;
         for (int j0 = 0; j0 < p.r; j0 += C::kRows) {
             const int rows = min(C::kRows, p.r - j0), tiles = (rows + 15) >> 4;
             float acc[C::kTiles][C::kOctets][4] = {};
-            const uint16_t* ar = A + ((int64_t)a * p.r + j0) * p.K;
             if (n) {
-#pragma unroll 2
-                for (int k0 = kb; k0 < ke; k0 += 32) {
-                    const int k = k0 + 8 * c;
-                    const bool in = k < ke;
-                    uint4 bv[C::kOctets];
+                const uint16_t* ar[2 * C::kTiles];
 #pragma unroll
-                    for (int o = 0; o < C::kOctets; ++o) {
-                        bv[o] = make_uint4(0, 0, 0, 0);
-                        if (in && 8 * o + gq < n) bv[o] = __ldg(reinterpret_cast<const uint4*>(xr[o] + k));
+                for (int q = 0; q < 2 * C::kTiles; ++q)
+                    ar[q] = A + ((int64_t)a * p.r + j0 + (q * 8 + gq < rows ? q * 8 + gq : gq)) * p.K + 8 * c;
+                // a step's operands load while the step before is multiplied; only a last, partial
+                // step looks at the end of K
+                uint4 bv[2][C::kOctets], av[2][2 * C::kTiles];
+                auto load = [&](int b, int k) {
+                    if (k + 32 <= ke) {
+#pragma unroll
+                        for (int o = 0; o < C::kOctets; ++o) bv[b][o] = __ldg(reinterpret_cast<const uint4*>(xr[o] + k));
+#pragma unroll
+                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = __ldg(reinterpret_cast<const uint4*>(ar[q] + k));
+                    } else {
+                        const bool in = k + 8 * c < ke;
+#pragma unroll
+                        for (int o = 0; o < C::kOctets; ++o) bv[b][o] = load_or_zero(xr[o] + k, in);
+#pragma unroll
+                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = load_or_zero(ar[q] + k, in);
                     }
+                };
+                auto multiply = [&](int b) {
 #pragma unroll
                     for (int q = 0; q < C::kTiles; ++q) {
-                        if (q >= tiles) break;
-                        const int r0 = q * 16 + gq;
-                        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                        if (in && r0 < rows) lo = __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)r0 * p.K + k));
-                        if (in && r0 + 8 < rows) hi = __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)(r0 + 8) * p.K + k));
+                        const uint4 lo = av[b][2 * q], hi = av[b][2 * q + 1];
                         const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
+                        if (q < tiles) {
 #pragma unroll
-                        for (int o = 0; o < C::kOctets; ++o) {
-                            if (o >= octets) break;
-                            mma16<BF16>(acc[q][o], f0, bv[o].x, bv[o].y);
-                            mma16<BF16>(acc[q][o], f1, bv[o].z, bv[o].w);
+                            for (int o = 0; o < C::kOctets; ++o) {
+                                mma16<BF16>(acc[q][o], f0, bv[b][o].x, bv[b][o].y);
+                                mma16<BF16>(acc[q][o], f1, bv[b][o].z, bv[b][o].w);
+                            }
                         }
                     }
+                };
+                load(0, kb);
+                for (int k0 = kb; k0 < ke; k0 += 64) {
+                    if (k0 + 32 < ke) load(1, k0 + 32);
+                    multiply(0);
+                    if (k0 + 64 < ke) load(0, k0 + 64);
+                    if (k0 + 32 < ke) multiply(1);
                 }
             }
             __syncthreads();  // the last pass's sums have been read
@@ -146,107 +162,145 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArg
     }
     if (p.slices > 1) tc::cluster_sync();
     else __syncthreads();
-    // each CTA finishes its share of the tokens, a warp a token
-    const int quads = p.r >> 2;
+    // each CTA finishes its share of the tokens: a warp a token, a lane every 32nd rank value
     for (int m = slice * 8 + warp; m < WIN; m += 8 * p.slices) {
         const int a = __shfl_sync(0xffffffffu, id, m);
         if (a < 0) continue;
         const float sc = p.scale ? __ldg(&p.scale[a]) : 1.0f;
-        float4 v[2];  // quads lane, lane + 32 (rank <= 256)
-        float most = 0.f;
+        constexpr int kPer = kMaxAdapterRank / 32;
+        float v[kPer], most = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int q = lane + 32 * i;
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (q < quads) {
-                const float* at = sums + m * p.r + 4 * q;
-                if (p.slices == 1) {
-                    v[i] = *reinterpret_cast<const float4*>(at);
-                } else {
-                    for (int s = 0; s < p.slices; ++s) {
-                        const float4 u = tc::ld_cluster4(tc::cluster_addr(at, s));
-                        v[i].x += u.x, v[i].y += u.y, v[i].z += u.z, v[i].w += u.w;
-                    }
-                }
-                v[i].x *= sc, v[i].y *= sc, v[i].z *= sc, v[i].w *= sc;
+        for (int i = 0; i < kPer; ++i) {
+            const int j = lane + 32 * i;
+            v[i] = 0.f;
+            if (32 * i >= p.r) break;
+            if (j < p.r) {
+                const float* at = sums + m * p.r + j;
+                if (p.slices == 1) v[i] = *at;
+                else
+                    for (int s = 0; s < p.slices; ++s) v[i] += tc::ld_cluster(tc::cluster_addr(at, s));
+                v[i] *= sc;
             }
-            most = fmaxf(fmaxf(fmaxf(most, fabsf(v[i].x)), fmaxf(fabsf(v[i].y), fabsf(v[i].z))), fabsf(v[i].w));
+            most = fmaxf(most, fabsf(v[i]));
         }
+        const int64_t row = (int64_t)(t0 + m) * p.r;
         if (TERMS == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (lane + 32 * i < quads)
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.v) + (int64_t)(t0 + m) * p.r + 4 * (lane + 32 * i)) = v[i];
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < p.r) static_cast<float*>(p.v)[row + lane + 32 * i] = v[i];
             continue;
         }
         float scale = 1.f;
         if (!BF16) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);  // biased exponent
-            scale = __uint_as_float((uint32_t)(254 - e) << 23);
-            if (lane == 0) adapter_back(p, TERMS)[t0 + m] = __uint_as_float((uint32_t)e << 23);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int q = lane + 32 * i;
-            if (q >= quads) continue;
-            float4 u = v[i];
-            if (!BF16) u.x *= scale, u.y *= scale, u.z *= scale, u.w *= scale;
-            uint4 o;
-            o.x = take_term<BF16>(u.x, u.y);
-            o.y = take_term<BF16>(u.z, u.w);
-            o.z = take_term<BF16>(u.x, u.y);
-            o.w = take_term<BF16>(u.z, u.w);
-            uint4* dst = static_cast<uint4*>(p.v) + ((int64_t)(t0 + m) * quads + q) * (TERMS == 3 ? 2 : 1);
-            dst[0] = o;
-            if (TERMS == 3) {
-                o.x = take_term<BF16>(u.x, u.y);
-                o.y = take_term<BF16>(u.z, u.w);
-                dst[1] = make_uint4(o.x, o.y, 0, 0);
+            float back = 1.f;
+            if (most != 0.f && !(most >= 0.25f && most < 32768.f)) {
+                const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);  // biased exponent
+                scale = __uint_as_float((uint32_t)(254 - e) << 23);
+                back = __uint_as_float((uint32_t)e << 23);
             }
+            if (lane == 0) adapter_back(p, TERMS)[t0 + m] = back;
+        }
+        uint16_t* out = static_cast<uint16_t*>(p.v) + row + lane;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (32 * i >= p.r) break;
+            if (lane + 32 * i >= p.r) continue;
+            float u = BF16 ? v[i] : v[i] * scale;
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) out[(int64_t)k * p.T * p.r + 32 * i] = take_term<BF16>(u);
         }
     }
     if (p.slices > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------- the delta alone
-// CTA: 128 features (32 a warp) by 32 tokens, 16 at a time, in fragments.
+// CTA: 16 tokens by 256 features, a warp 64 of them.  Tokens are the MMA's M, so
+// that a lane holds pairs of adjacent features: y moves in 8-byte (fp32) or
+// 4-byte pieces that fill 32-byte sectors, and v's fragments serve all 64
+// features.  Everything independent of v is loaded before the wait for it.
 template <bool BF16, bool OUT32>
 __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f0 = blockIdx.x * 128 + warp * 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int TERMS = BF16 && OUT32 ? 3 : 2, NT = 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
+    const int f0 = (blockIdx.y * 4 + warp) * 64, t0 = blockIdx.x * 16, n = min(16, p.T - t0);
     if (f0 >= p.N) return;
-    const int end = min(p.T, ((int)blockIdx.y + 1) * 32);
-    for (int t0 = blockIdx.y * 32; t0 < end; t0 += 16) {
-        const int n = min(16, end - t0);
-        uint32_t r[2][8];
+    int id = lane < n ? __ldg(&p.ids[t0 + lane]) : -1;
+    if (id < 0 || id >= p.L) id = -1;
+    const uint32_t mine = __match_any_sync(0xffffffffu, id);
+    uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
+    float y[NT][4];  // [8 features][token gq: features 2c, 2c + 1; token gq + 8: the same]
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = frag_token(i >> 2, i), f = f0 + frag_feature(m, i & 3);
-                float v = 0.f;
-                if (p.accumulate && t < n && f < p.N) {
-                    const int64_t o = (int64_t)(t0 + t) * p.ldy + f;
-                    v = OUT32 ? static_cast<const float*>(p.y)[o] : unpack1<BF16>(static_cast<const uint16_t*>(p.y)[o]);
-                }
-                r[m][i] = __float_as_uint(v);
+        for (int h = 0; h < 2; ++h) {
+            const int f = f0 + 8 * t + 2 * c;
+            float2 v = make_float2(0.f, 0.f);
+            if (p.accumulate && gq + 8 * h < n && f < p.N) {
+                const int64_t o = (int64_t)(t0 + gq + 8 * h) * p.ldy + f;
+                if (OUT32) v = *reinterpret_cast<const float2*>(static_cast<const float*>(p.y) + o);
+                else v = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.y) + o));
             }
-        add_delta<BF16, BF16 && OUT32 ? 3 : 2>(p, t0, n, f0, r[0], r[1]);
+            y[t][2 * h] = v.x;
+            y[t][2 * h + 1] = v.y;
+        }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int quads = p.r >> 2;
+    while (todo) {  // one pass per distinct adapter of the 16 tokens
+        const int leader = __ffs(todo) - 1;
+        const int a = __shfl_sync(0xffffffffu, id, leader);
+        const uint32_t used = __shfl_sync(0xffffffffu, mine, leader);
+        todo &= ~used;
+        const bool use[2] = {((used >> gq) & 1) != 0, ((used >> (8 + gq)) & 1) != 0};
+        const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)a * p.N + f0 + gq) * p.r;
+        const int64_t vrow = (int64_t)(t0 + gq) * p.r;
+        float d[NT][4] = {};
+#pragma unroll 2
+        for (int q0 = 0; q0 < quads; q0 += 4) {
+            const int q = q0 + c;
+            uint2 v[2][TERMS], w[NT];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int t = 0; t < NT; ++t)
+                w[t] = q < quads && f0 + 8 * t + gq < p.N ? __ldg(reinterpret_cast<const uint2*>(B + (int64_t)8 * t * p.r + 4 * q))
+                                                          : make_uint2(0, 0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = frag_token(i >> 2, i), f = f0 + frag_feature(m, i & 3);
-                if (t < n && f < p.N) {
-                    const int64_t o = (int64_t)(t0 + t) * p.ldy + f;
-                    if (OUT32) static_cast<float*>(p.y)[o] = __uint_as_float(r[m][i]);
-                    else static_cast<uint16_t*>(p.y)[o] = pack1<BF16>(__uint_as_float(r[m][i]));
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k) {
+                    v[h][k] = make_uint2(0, 0);
+                    if (q < quads && use[h])
+                        v[h][k] = *reinterpret_cast<const uint2*>(adapter_term(p, k) + vrow + (int64_t)h * 8 * p.r + 4 * q);
                 }
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+                const uint32_t av[4] = {v[0][k].x, v[1][k].x, v[0][k].y, v[1][k].y};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16<BF16>(d[t], av, w[t].x, w[t].y);
             }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!use[h]) continue;  // (another adapter's infinities must not reach this token)
+            const float back = BF16 ? 1.f : adapter_back(p, TERMS)[t0 + gq + 8 * h];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                y[t][2 * h] += BF16 ? d[t][2 * h] : d[t][2 * h] * back;
+                y[t][2 * h + 1] += BF16 ? d[t][2 * h + 1] : d[t][2 * h + 1] * back;
+            }
+        }
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int f = f0 + 8 * t + 2 * c;
+            if (gq + 8 * h < n && f < p.N) {
+                const int64_t o = (int64_t)(t0 + gq + 8 * h) * p.ldy + f;
+                if (OUT32) *reinterpret_cast<float2*>(static_cast<float*>(p.y) + o) = make_float2(y[t][2 * h], y[t][2 * h + 1]);
+                else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + o) = pack2<BF16>(y[t][2 * h], y[t][2 * h + 1]);
+            }
+        }
 }
 
 // ---------------------------------------------------------------- launcher
@@ -264,8 +318,8 @@ static int shrink_slices(int T, int K) {
 }
 
 size_t adapter_workspace(int T, int r) {
-    // the largest form: two 16-byte vectors per four rank values, and a factor per token
-    return (size_t)T * (r / 4) * 32 + (((size_t)T * 4 + 15) & ~size_t(15));
+    // the largest form: three 16-bit terms per rank value, and a factor per token
+    return (size_t)T * r * 6 + (((size_t)T * 4 + 15) & ~size_t(15));
 }
 
 template <bool BF16, int WIN, int TERMS>
@@ -305,7 +359,7 @@ static cudaError_t adapters(AdapterArgs p, cudaStream_t s) {
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((p.N + 127) / 128, (p.T + 31) / 32);
+    cfg.gridDim = dim3((p.T + 15) / 16, (p.N + 255) / 256);
     cfg.blockDim = 128;
     cfg.stream = s;
     cfg.attrs = &at;

@@ -47,4 +47,16 @@ MOE_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t 
     else mma_f16(d, a, b0, b1, d);
 }
 
+// 16 bytes through the read-only path, or zeros: a predicated load, not a
+// branch, so that independent loads stay together (not volatile: they may move
+// ahead of earlier MMAs)
+MOE_DEV uint4 load_or_zero(const void* p, bool take) {
+    uint4 v;
+    asm("{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n"
+        " mov.b32 %3, 0;\n @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p), "r"(take ? 1 : 0));
+    return v;
+}
+
 }  // namespace moe

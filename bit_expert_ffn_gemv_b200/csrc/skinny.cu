@@ -40,34 +40,48 @@ MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t*
     float acc[NB][4] = {};
     const uint16_t* xr[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) xr[b] = x + (int64_t)min(b * 8 + gq, n - 1) * ldx;
-    constexpr int U = 4;  // 32-wide steps in flight
-    for (int k0 = kb; k0 < ke; k0 += 32 * U) {
-        uint4 lo[U], hi[U];
+    for (int b = 0; b < NB; ++b) xr[b] = x + (int64_t)min(b * 8 + gq, n - 1) * ldx + 8 * c;
+    w0 += 8 * c;
+    w1 += 8 * c;
+    constexpr int U = NB <= 2 ? 8 : 4;  // 32-wide steps in flight
+    uint4 lo[U], hi[U];
+    auto multiply = [&](int u, const uint4 (&bv)[NB]) {
+        const uint32_t f0[4] = {lo[u].x, hi[u].x, lo[u].y, hi[u].y}, f1[4] = {lo[u].z, hi[u].z, lo[u].w, hi[u].w};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            mma16<BF16>(acc[b], f0, bv[b].x, bv[b].y);
+            mma16<BF16>(acc[b], f1, bv[b].z, bv[b].w);
+        }
+    };
+    int k0 = kb;
+    for (; k0 + 32 * U <= ke; k0 += 32 * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = k0 + 32 * u + 8 * c;
-            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-            if (k < ke) {
-                lo[u] = __ldcs(reinterpret_cast<const uint4*>(w0 + k));
-                hi[u] = __ldcs(reinterpret_cast<const uint4*>(w1 + k));
-            }
+            lo[u] = __ldcs(reinterpret_cast<const uint4*>(w0 + k0 + 32 * u));
+            hi[u] = __ldcs(reinterpret_cast<const uint4*>(w1 + k0 + 32 * u));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = k0 + 32 * u + 8 * c;
             uint4 bv[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                bv[b] = make_uint4(0, 0, 0, 0);
-                if (k < ke) bv[b] = __ldg(reinterpret_cast<const uint4*>(xr[b] + k));
-            }
-            const uint32_t f0[4] = {lo[u].x, hi[u].x, lo[u].y, hi[u].y}, f1[4] = {lo[u].z, hi[u].z, lo[u].w, hi[u].w};
+            for (int b = 0; b < NB; ++b) bv[b] = __ldg(reinterpret_cast<const uint4*>(xr[b] + k0 + 32 * u));
+            multiply(u, bv);
+        }
+    }
+    if (k0 < ke) {  // the rest, zeros past the end
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                mma16<BF16>(acc[b], f0, bv[b].x, bv[b].y);
-                mma16<BF16>(acc[b], f1, bv[b].z, bv[b].w);
-            }
+        for (int u = 0; u < U; ++u) {
+            const bool in = k0 + 32 * u + 8 * c < ke;
+            lo[u] = load_or_zero(w0 + k0 + 32 * u, in);
+            hi[u] = load_or_zero(w1 + k0 + 32 * u, in);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + 32 * u >= ke) break;
+            uint4 bv[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) bv[b] = load_or_zero(xr[b] + k0 + 32 * u, k0 + 32 * u + 8 * c < ke);
+            multiply(u, bv);
         }
     }
     // [feature][row]
@@ -80,9 +94,10 @@ MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t*
     }
 }
 
-template <bool BF16, bool OUT32, bool ADAPT>
+// MAXNB: blocks of 8 rows that a group can have (the call's rows, rounded up)
+template <bool BF16, bool OUT32, bool ADAPT, int MAXNB>
 __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyArgs p) {
-    constexpr int kPitch = kSkinnyMaxRows + 1;
+    constexpr int kPitch = 8 * MAXNB + 1;
     __shared__ __align__(16) float red[8][16 * kPitch];
     __shared__ int found[3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
@@ -112,12 +127,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
     const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)row0 * p.ldx;
     const int kw = (((p.K + 7) >> 3) + 31) & ~31, kb = warp * kw, ke = min(p.K, kb + kw);
     if (n <= 8) skinny_sums<BF16, 1>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
-    else if (n <= 16) skinny_sums<BF16, 2>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
-    else if (n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
-    else skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (MAXNB == 2 || (MAXNB > 2 && n <= 16)) skinny_sums<BF16, 2>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (MAXNB == 8 && n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (MAXNB == 8) skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     __syncthreads();
     // thread: feature tid % 16, rows tid / 16 + 16 i
-    constexpr int kOut = 16 * kSkinnyMaxRows / kSkinnyThreads;
+    constexpr int kOut = (16 * 8 * MAXNB + kSkinnyThreads - 1) / kSkinnyThreads;
     const int j = tid & 15, f = f0 + j, m0 = tid >> 4;
     float s[kOut];
 #pragma unroll
@@ -148,7 +163,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
         asm volatile("griddepcontrol.wait;" ::: "memory");
         constexpr int kBlock = 64;  // rank values per pass
         float* v = &red[0][0];      // [row][kBlock]: the sums above are in registers
-        static_assert(kSkinnyMaxRows * kBlock <= 8 * 16 * kPitch, "v fits over the sums");
+        static_assert(8 * MAXNB * kBlock <= 8 * 16 * kPitch, "v fits over the sums");
         for (int j0 = 0; j0 < ad.r; j0 += kBlock) {
             const int nj = min(kBlock, ad.r - j0), quads = nj >> 2;
             __syncthreads();
@@ -185,6 +200,23 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
     }
 }
 
+template <bool BF16, bool OUT32, bool ADAPT>
+static cudaError_t skinny(const SkinnyArgs& p, int rows, dim3 grid, cudaStream_t s) {
+    auto kern = rows <= 8    ? skinny_kernel<BF16, OUT32, ADAPT, 1>
+                : rows <= 16 ? skinny_kernel<BF16, OUT32, ADAPT, 2>
+                             : skinny_kernel<BF16, OUT32, ADAPT, 8>;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = kSkinnyThreads;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = ADAPT ? 1 : 0;  // behind the inner values' kernel
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const void* x, int64_t ldx, bool out32,
                                   cudaStream_t s) {
     SkinnyArgs p{};
@@ -199,14 +231,8 @@ cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const voi
     p.y = g.out;
     p.ldy = g.ldo;
     const dim3 grid((g.F + 15) / 16, g.M);
-    if (g.bf16) {
-        if (out32) skinny_kernel<true, true, false><<<grid, kSkinnyThreads, 0, s>>>(p);
-        else skinny_kernel<true, false, false><<<grid, kSkinnyThreads, 0, s>>>(p);
-    } else {
-        if (out32) skinny_kernel<false, true, false><<<grid, kSkinnyThreads, 0, s>>>(p);
-        else skinny_kernel<false, false, false><<<grid, kSkinnyThreads, 0, s>>>(p);
-    }
-    return cudaGetLastError();
+    if (g.bf16) return out32 ? skinny<true, true, false>(p, g.M, grid, s) : skinny<true, false, false>(p, g.M, grid, s);
+    return out32 ? skinny<false, true, false>(p, g.M, grid, s) : skinny<false, false, false>(p, g.M, grid, s);
 }
 
 cudaError_t launch_skinny_adapter(const AdapterArgs& a, bool bf16, bool out32, cudaStream_t s) {
@@ -219,20 +245,9 @@ cudaError_t launch_skinny_adapter(const AdapterArgs& a, bool bf16, bool out32, c
     p.y = a.y;
     p.ldy = a.ldy;
     p.ad = a;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((a.N + 15) / 16);
-    cfg.blockDim = kSkinnyThreads;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    if (bf16)
-        return out32 ? cudaLaunchKernelEx(&cfg, skinny_kernel<true, true, true>, p)
-                     : cudaLaunchKernelEx(&cfg, skinny_kernel<true, false, true>, p);
-    return out32 ? cudaLaunchKernelEx(&cfg, skinny_kernel<false, true, true>, p)
-                 : cudaLaunchKernelEx(&cfg, skinny_kernel<false, false, true>, p);
+    const dim3 grid((a.N + 15) / 16);
+    if (bf16) return out32 ? skinny<true, true, true>(p, a.T, grid, s) : skinny<true, false, true>(p, a.T, grid, s);
+    return out32 ? skinny<false, true, true>(p, a.T, grid, s) : skinny<false, false, true>(p, a.T, grid, s);
 }
 
 }  // namespace moe

@@ -82,6 +82,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libmoe.so (built by bit_expert_ffn_gemv_b200.build); raise if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):

@@ -101,13 +101,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
 #pragma unroll
                         for (int o = 0; o < C::kOctets; ++o) bv[b][o] = __ldg(reinterpret_cast<const uint4*>(xr[o] + k));
 #pragma unroll
-                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = __ldg(reinterpret_cast<const uint4*>(ar[q] + k));
+                        for (int q = 0; q < 2 * C::kTiles; ++q)
+                            if (q < 2 * tiles) av[b][q] = __ldg(reinterpret_cast<const uint4*>(ar[q] + k));
                     } else {
                         const bool in = k + 8 * c < ke;
 #pragma unroll
                         for (int o = 0; o < C::kOctets; ++o) bv[b][o] = load_or_zero(xr[o] + k, in);
 #pragma unroll
-                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = load_or_zero(ar[q] + k, in);
+                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = load_or_zero(ar[q] + k, in && q < 2 * tiles);
                     }
                 };
                 auto multiply = [&](int b) {

@@ -327,9 +327,10 @@ template <bool BF16, int WIN, int TERMS>
 static cudaError_t shrink(const AdapterArgs& p, cudaStream_t s) {
     auto kern = shrink_kernel<BF16, WIN, TERMS>;
     const int smem = ShrinkCfg<WIN>::kRed + WIN * p.r * 4;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         ShrinkCfg<WIN>::kRed + WIN * kMaxAdapterRank * 4);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 1;

@@ -82,18 +82,20 @@ struct GroupedTile {
 };
 
 // The tile list.  Forward and rows products cut a group into blocks of equal
-// size (at most 256 rows, multiples of 32, so that no block is a sliver) and
+// size (at most g.block rows, 256 or less where that fills the GPU; multiples of 32, so that no block is a sliver) and
 // enumerate (group, band of blocks, features, block); the weight gradient, with
 // 256-wide k columns in the blocks' place, the same.
 struct TileList {
     const int* start;  // [E + 1] first row of each group
     const int* pre;    // [E + 1] forward, rows: blocks of the groups before this place
     const int* order;  // [E] group at each place
+    int E;
 };
 
-// rows of each block of a group of c rows
-MOE_DEV int block_rows(int c) {
-    const int blocks = (c + 255) >> 8;
+// blocks of a group of c rows, and the rows of each
+MOE_DEV int block_count(int c, int most) { return (c + most - 1) / most; }
+MOE_DEV int block_rows(int c, int most) {
+    const int blocks = block_count(c, most);
     return blocks <= 1 ? c : (((c + blocks - 1) / blocks) + 31) & ~31;
 }
 
@@ -123,7 +125,7 @@ MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const TileList& l, int 
     }
     const int q = t / JT;
     r.g0 = 0;
-    int lo = 0, hi = g.E - 1;  // last place with pre <= q
+    int lo = 0, hi = l.E - 1;  // last place with pre <= q
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (l.pre[mid] <= q) lo = mid;
@@ -133,7 +135,7 @@ MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const TileList& l, int 
     band(t - l.pre[lo] * JT, JT, l.pre[lo + 1] - l.pre[lo], jt, at);
     r.f0 = jt << 8;
     r.e = l.order[lo];
-    const int c = l.start[r.e + 1] - l.start[r.e], rows = block_rows(c);
+    const int c = l.start[r.e + 1] - l.start[r.e], rows = block_rows(c, g.block);
     at *= rows;
     r.row0 = l.start[r.e] + at;
     r.n = min(rows, c - at);
@@ -166,9 +168,31 @@ MOE_DEV int block_exclusive(int v, int start, int* wsum) {
     return ex;
 }
 
+// Adapters (one "group" per run of tokens of one adapter, below): the maps of B
+// [L][N][r] and of v's terms [term][T][r], in boxes of 128 and of 32 tokens.
+template <bool ADAPT>
+struct GroupedExtra {};
+template <>
+struct GroupedExtra<true> {
+    AdapterArgs args;
+    CUtensorMap b, v, v_small;
+};
+
+// Tokens [row0, row0 + n) whose v's terms are unscaled (fp16; adapter.cuh); a warp.
+MOE_DEV bool unscaled(const AdapterArgs& p, int terms, int row0, int n) {
+    const float* back = adapter_back(p, terms) + row0;
+    bool ok = true;
+    for (int i = threadIdx.x & 31; i < n; i += 32) ok = ok && back[i] == 1.f;
+    return __all_sync(0xffffffffu, ok);
+}
+MOE_DEV int adapter_of(const AdapterArgs& p, int t) {
+    const int id = __ldg(&p.ids[t]);
+    return id >= 0 && id < p.L ? id : -1;
+}
+
 template <int MODE, bool OUT32, bool ADAPT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
-    grouped_kernel(const GroupedArgs g, const AdapterArgs ad, const __grid_constant__ CUtensorMap amap,
+    grouped_kernel(const GroupedArgs g, const __grid_constant__ GroupedExtra<ADAPT> ex, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap) {
     constexpr bool WG = MODE == kGroupedWeights;
     extern __shared__ uint8_t smem_raw[];
@@ -196,29 +220,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     }
     if (warp == 2) tc::tmem_alloc_pair(&tmem_slot, 512);
 
-    // Group starts: clamped into [0, rows] and made ascending by a running
-    // maximum, so that a bad table reads and writes nothing out of range.
     constexpr int kPer = kGroupedMaxGroups / kGroupedThreads;
-    const int first = ADAPT ? 0 : min(max(__ldg(&g.offsets[0]), 0), g.M);
-    int end[kPer], top = first;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        if (e < g.E) top = max(top, ADAPT ? g.M : min(max(__ldg(&g.offsets[e + 1]), 0), g.M));
-        end[i] = top;
-    }
-    const int top_before = block_exclusive<true>(top, first, wsum);
-    int begin = max(top_before, first);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i, stop = max(end[i], begin);
-        if (e < g.E) {
-            start[e] = begin;
-            // the sort key: rows of one tile
-            order[e] = WG ? stop - begin : block_rows(stop - begin);
+    int E = g.E;
+    bool runs = false;  // adapters: every tile has one adapter
+    if constexpr (ADAPT) {
+        // Groups are the runs of tokens of one adapter (or of none), so that the
+        // tensor core can add a tile's delta: worth it while runs are 32 tokens
+        // long on average.  Otherwise one group, and the epilogue adds the deltas.
+        const int seg = (g.M + kGroupedThreads - 1) / kGroupedThreads;
+        const int i0 = min(tid * seg, g.M), i1 = min(i0 + seg, g.M);
+        int n = 0, was = i0 > 0 && i0 < i1 ? adapter_of(ex.args, i0 - 1) : -2;
+        const int before0 = was;
+#pragma unroll 8
+        for (int i = i0; i < i1; ++i) {
+            const int id = adapter_of(ex.args, i);
+            n += id != was;
+            was = id;
         }
-        if (e == g.E - 1) start[g.E] = stop;
-        begin = stop;
+        int at = block_exclusive<false>(n, 0, wsum);
+        if (tid == kGroupedThreads - 1) pre[0] = at + n;
+        __syncthreads();
+        const int found = pre[0];
+        runs = found <= kGroupedMaxGroups && (int64_t)found * 32 <= g.M;
+        E = runs ? found : 1;
+        if (runs) {
+            was = before0;
+            for (int i = i0; i < i1; ++i) {
+                const int id = adapter_of(ex.args, i);
+                if (id != was) start[at++] = i;
+                was = id;
+            }
+        }
+        if (tid == 0) {
+            if (!runs) start[0] = 0;
+            start[E] = g.M;
+        }
+    } else {
+        // Group starts: clamped into [0, rows] and made ascending by a running
+        // maximum, so that a bad table reads and writes nothing out of range.
+        const int first = min(max(__ldg(&g.offsets[0]), 0), g.M);
+        int end[kPer], top = first;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i;
+            if (e < E) top = max(top, min(max(__ldg(&g.offsets[e + 1]), 0), g.M));
+            end[i] = top;
+        }
+        const int top_before = block_exclusive<true>(top, first, wsum);
+        int begin = max(top_before, first);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i, stop = max(end[i], begin);
+            if (e < E) {
+                start[e] = begin;
+                order[e] = WG ? stop - begin : block_rows(stop - begin, g.block);  // the sort key: rows of one tile
+            }
+            if (e == E - 1) start[E] = stop;
+            begin = stop;
+        }
     }
     __syncthreads();
     // Places by falling tile cost, so that the long tiles come first and the
@@ -226,15 +285,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     // matrices is the cost (under 256 rows on average), the groups' own order,
     // which mixes short and long tiles and keeps HBM busy throughout.
     int place[kPer];
-    const bool sorted = !ADAPT && (WG || start[g.E] - start[0] >= 256 * g.E);
+    const bool sorted = !ADAPT && (WG || start[E] - start[0] >= 256 * E);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
         place[i] = e;
-        if (sorted && e < g.E) {
+        if (sorted && e < E) {
             const int key = order[e];
             int n = 0;
-            for (int o = 0; o < g.E; ++o) {
+            for (int o = 0; o < E; ++o) {
                 const int k = order[o];
                 n += k > key || (k == key && o < e);
             }
@@ -244,32 +303,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        if (tid * kPer + i < g.E) order[place[i]] = tid * kPer + i;
+        if (tid * kPer + i < E) order[place[i]] = tid * kPer + i;
     __syncthreads();
     int total;
     if (WG) {
-        total = g.E * JT * ((g.C + 255) >> 8);
+        total = E * JT * ((g.C + 255) >> 8);
     } else {
         int mine = 0, blocks[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int at = tid * kPer + i;
-            const int e = at < g.E ? order[at] : 0;
-            blocks[i] = at < g.E ? (start[e + 1] - start[e] + 255) >> 8 : 0;
+            const int e = at < E ? order[at] : 0;
+            blocks[i] = at < E ? block_count(start[e + 1] - start[e], g.block) : 0;
             mine += blocks[i];
         }
         int before = block_exclusive<false>(mine, 0, wsum);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int at = tid * kPer + i;
-            if (at < g.E) pre[at] = before;
+            if (at < E) pre[at] = before;
             before += blocks[i];
-            if (at == g.E - 1) pre[g.E] = before;
+            if (at == E - 1) pre[E] = before;
         }
         __syncthreads();
-        total = pre[g.E] * JT;
+        total = pre[E] * JT;
     }
-    const TileList list{start, pre, order};
+    const TileList list{start, pre, order, E};
     tc::fence_before();
     __syncthreads();
     tc::cluster_sync();  // both CTAs' barriers are initialised, both halves of tensor memory allocated
@@ -277,6 +336,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     const uint32_t tmem = tmem_slot;
     const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
     const int KC = (g.C + 63) >> 6;  // steps per tile (forward, rows)
+    // Adapters: steps that add a tile's delta, v's terms times B in 64-wide
+    // blocks of the rank; 0 where there is none or the epilogue adds it.  Whole
+    // warps.  (fp16: v must be there to see whether it was scaled.)
+    constexpr int kTerms = OUT32 ? 3 : 2;  // fp16: always 2
+    int rank_blocks = 0, terms = 0, one_adapter = -1;
+    if constexpr (ADAPT) {
+        rank_blocks = (ex.args.r + 63) >> 6;
+        terms = g.bf16 ? kTerms : 2;
+    }
+    auto delta_steps = [&](const GroupedTile& tl) -> int {
+        if constexpr (ADAPT) {
+            one_adapter = runs ? adapter_of(ex.args, tl.row0) : -1;
+            if (one_adapter < 0) return 0;
+            if (!g.bf16) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                if (!unscaled(ex.args, terms, tl.row0, tl.n)) return 0;
+            }
+            return terms * rank_blocks;
+        }
+        return 0;
+    };
 
     if (warp == 0 || warp == 3) {
         // ======================= loaders (the whole warp walks, one lane issues): warp 0 A, warp 3 B
@@ -287,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         uint32_t phase = 1;  // parity of the stage's last "empty" (0 once every stage has been used)
         for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
             const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
-            const int KS = WG ? (tl.n + 63) >> 6 : KC;
+            const int KS = WG ? (tl.n + 63) >> 6 : KC + delta_steps(tl);
             const int nh = WG ? 128 : ((tl.n + 31) & ~31) >> 1;
             const int brow = tl.row0 + (int)rank * nh;
             const int f = tl.f0 + (int)rank * 128, gc = tl.g0 + (int)rank * 128;
@@ -301,6 +381,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 // a last step that ends inside 16 rows is completed by warp 2 once it is cleared
                 const bool tail = WG && s == KS - 1 && (tl.n & 15);
                 const uint32_t bar = (tail ? tail_own : full_leader) + (uint32_t)st * 8u;
+                if (ADAPT && s == KC) {
+                    asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
+                    fence_proxy_async_global();
+                }
                 if (one) {
                     if (tail) mbar_arrive_expect_tx(&tail_bar[st], bytes);
                     else tc::arrive_expect_cluster(bar, bytes);
@@ -313,9 +397,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                             tc::tma_2d_pair(Bs, &bmap, gc, r, bar);
                             tc::tma_2d_pair(Bs + kPanel, &bmap, gc + 64, r, bar);
                         }
+                    } else if (ADAPT && s >= KC) {
+                        if constexpr (ADAPT) {
+                            const int term = (s - KC) / rank_blocks, j = (s - KC) % rank_blocks * 64;
+                            if (is_a) tc::tma_3d_pair(As, &ex.b, j, f, one_adapter, bar);
+                            else if (nbox == 0) tc::tma_3d_pair(Bs, &ex.v, j, brow, term, bar);
+                            else
+                                for (int x = 0; x < nbox; ++x)
+                                    tc::tma_3d_pair(Bs + x * 32 * 128, &ex.v_small, j, brow + x * 32, term, bar);
+                        }
                     } else if (is_a) {
                         if (MODE == kGroupedForward) {
-                            tc::tma_3d_pair(As, &amap, s * 64, f, tl.e, bar);
+                            tc::tma_3d_pair(As, &amap, s * 64, f, ADAPT ? 0 : tl.e, bar);  // (adapters: one W)
                         } else {
                             tc::tma_3d_pair(As, &amap, f, s * 64, tl.e, bar);
                             tc::tma_3d_pair(As + kPanel, &amap, f + 64, s * 64, tl.e, bar);
@@ -350,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             uint32_t phase = 0;
             for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
                 const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
-                const int KS = WG ? (tl.n + 63) >> 6 : KC;
+                const int KS = WG ? (tl.n + 63) >> 6 : KC + delta_steps(tl);
                 const uint32_t idesc = tc::idesc_f16_major(256, WG ? 256 : (tl.n + 31) & ~31, g.bf16 != 0,
                                                            MODE != kGroupedForward, WG);
                 for (int s = 0; s < KS; ++s) {
@@ -364,13 +457,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     tc::fence_after();
                     const uint32_t acc = tmem + (it & 1) * 256;
                     const uint64_t ad = adesc + (uint32_t)(st * (kGroupedStage >> 4)), bd = bdesc + (uint32_t)(st * (kGroupedStage >> 4));
-                    const int kks = WG && s == KS - 1 ? (tl.n - s * 64 + 15) >> 4 : 4;
+                    int kks = WG && s == KS - 1 ? (tl.n - s * 64 + 15) >> 4 : 4;
+                    if constexpr (ADAPT) {
+                        if (s >= KC) kks = (min(64, ex.args.r - (s - KC) % rank_blocks * 64) + 15) >> 4;
+                    }
                     const bool done = s == KS - 1 || (OUT32 && ps == kPartSteps - 1);
                     if (one) {
                         tc::mma_pair(acc, ad, bd, idesc, ps > 0 ? 1u : 0u);
 #pragma unroll
                         for (int kk = 1; kk < 4; ++kk)
-                            if (!WG || kk < kks) tc::mma_pair(acc, ad + kk * kA16, bd + kk * kB16, idesc, 1u);
+                            if ((!WG && !ADAPT) || kk < kks) tc::mma_pair(acc, ad + kk * kA16, bd + kk * kB16, idesc, 1u);
                         tc::commit_pair(&empty_bar[st]);
                         if (done) tc::commit_pair(&accf_bar[it & 1]);
                     }
@@ -421,7 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
             const bool empty = WG && tl.n == 0;
             if (empty && g.accumulate) continue;
-            const int KS = WG ? (tl.n + 63) >> 6 : KC;
+            const int KS = WG ? (tl.n + 63) >> 6 : KC + delta_steps(tl);
+            const bool by_hand = ADAPT && KS == KC && (!runs || one_adapter >= 0);  // deltas to add here
             const int parts = OUT32 && !empty ? (KS + kPartSteps - 1) / kPartSteps : 1;
             for (int part = 0; part < parts; ++part) {
                 const int b = it & 1, use = it >> 1;
@@ -450,14 +547,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     tc::ld_frags_nowait(tb + (16u << 16), r[1]);
                     tc::ld_wait();
                     for (int c0 = 0; c0 < tl.n; c0 += 32) {
-                        if (ADAPT && part == 0) {
+                        if constexpr (ADAPT) {
+                            if (by_hand && part == 0)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (c0 + 16 * h < tl.n) {
-                                    const int m = min(16, tl.n - c0 - 16 * h);
-                                    if (bf16) add_delta<true, OUT32 ? 3 : 2>(ad, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
-                                    else add_delta<false, 2>(ad, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
-                                }
+                                for (int h = 0; h < 2; ++h)
+                                    if (c0 + 16 * h < tl.n) {
+                                        const int m = min(16, tl.n - c0 - 16 * h);
+                                        if (bf16) add_delta<true, kTerms>(ex.args, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
+                                        else add_delta<false, 2>(ex.args, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
+                                    }
                         }
                         if (ADAPT && !OUT32 && g.accumulate) {  // y's values, added before the one rounding
                             const uint16_t* y = static_cast<const uint16_t*>(g.out) + at + (int64_t)c0 * g.ldo;
@@ -611,6 +709,14 @@ static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t r
     return encode_tiles(m, elem16(bf16), base, 2, dims, str, box, 128);
 }
 
+// Rows per block: 256, less where that leaves SMs without a tile (a matrix read
+// by more blocks comes from L2).
+static int block_limit(int rows, int features) {
+    const int64_t JT = (features + 255) / 256, pairs = sm_count() / 2;
+    const int64_t even = (rows * JT / pairs + 31) / 32 * 32;
+    return (int)(even < 32 ? 32 : even > 256 ? 256 : even);
+}
+
 template <int MODE, bool OUT32>
 static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
     auto kern = grouped_kernel<MODE, OUT32, false>;
@@ -618,7 +724,7 @@ static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, in
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
-    kern<<<2 * pairs, kGroupedThreads, smem, s>>>(g, AdapterArgs{}, m.a, m.b, m.c);
+    kern<<<2 * pairs, kGroupedThreads, smem, s>>>(g, GroupedExtra<false>{}, m.a, m.b, m.c);
     return cudaGetLastError();
 }
 
@@ -649,11 +755,26 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     g.bf16 = bf16 ? 1 : 0;
     g.accumulate = p.accumulate;
     g.status = p.status;
+    g.block = block_limit(p.T, p.N);
+    GroupedExtra<true> ex;
+    ex.args = p;
+    {
+        const cuuint64_t bd[3] = {(cuuint64_t)p.r, (cuuint64_t)p.N, (cuuint64_t)p.L};
+        const cuuint64_t bs[2] = {(cuuint64_t)p.r * 2, (cuuint64_t)p.N * p.r * 2};
+        const cuuint64_t vd[3] = {(cuuint64_t)p.r, (cuuint64_t)p.T, bf16 && OUT32 ? 3u : 2u};
+        const cuuint64_t vs[2] = {(cuuint64_t)p.r * 2, (cuuint64_t)p.T * p.r * 2};
+        const cuuint32_t big[3] = {64, 128, 1}, small[3] = {64, 32, 1};
+        e = encode_tiles(&ex.b, elem16(bf16), p.b, 3, bd, bs, big, 128);
+        if (e == cudaSuccess) e = encode_tiles(&ex.v, elem16(bf16), p.v, 3, vd, vs, big, 128);
+        if (e == cudaSuccess) e = encode_tiles(&ex.v_small, elem16(bf16), p.v, 3, vd, vs, small, 128);
+        if (e != cudaSuccess) return e;
+    }
     auto kern = grouped_kernel<kGroupedForward, OUT32, true>;
     constexpr int smem = kGroupedSmem;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256);
+    // (runs cut blocks off: at most one block more per run of 32 tokens)
+    const int64_t tiles = (int64_t)((p.T + g.block - 1) / g.block + p.T / 32) * ((p.N + 255) / 256);
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
@@ -664,16 +785,18 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, g, p, m.a, m.b, m.c);
+    return cudaLaunchKernelEx(&cfg, kern, g, ex, m.a, m.b, m.c);
 }
 
 cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {
     return out32 ? adapter_launch<true>(p, bf16, s) : adapter_launch<false>(p, bf16, s);
 }
 
-cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const void* x, int64_t ldx, const void* dy,
+cudaError_t launch_grouped(int mode, const GroupedArgs& args, const void* w, const void* x, int64_t ldx, const void* dy,
                            int64_t lddy, bool out_fp32, cudaStream_t s) {
     GroupedMaps m{};
+    GroupedArgs g = args;
+    g.block = block_limit(g.M, g.F);
     const bool bf = g.bf16 != 0;
     cudaError_t e;
     const int JT = (g.F + 255) / 256;
@@ -695,7 +818,7 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const 
     e = product_maps(&m, forward, bf, g.E, forward ? g.F : g.C, forward ? g.C : g.F, w, forward ? x : dy, g.M,
                      forward ? ldx : lddy);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ((int64_t)(g.M + 255) / 256 + (g.E < g.M ? g.E : g.M)) * JT;
+    const int64_t tiles = ((int64_t)(g.M + g.block - 1) / g.block + (g.E < g.M ? g.E : g.M)) * JT;
     if (mode == kGroupedForward)
         return out_fp32 ? grouped_launch<kGroupedForward, true>(g, m, tiles, s)
                         : grouped_launch<kGroupedForward, false>(g, m, tiles, s);

@@ -177,7 +177,8 @@ struct GroupedArgs {
     void* out;
     int64_t ldo;             // row pitch of out in values (weights: K)
     int bf16;                // operands (and a 16-bit out) are bf16, else fp16
-    int accumulate;          // weights, fp32 out: add to out
+    int accumulate;          // add to out (weights: fp32 out)
+    int block;               // rows of a tile, at most (32..256)
     uint32_t* status;
 };
 cudaError_t launch_grouped(int mode, const GroupedArgs& g, const void* w, const void* x, int64_t ldx, const void* dy,

@@ -42,11 +42,14 @@ namespace moe {
 
 constexpr int kGroupedThreads = 256;
 constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an operand, one K = 64 step
-constexpr int kGroupedStage = 2 * kHalfTile;    // A half, B half
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
-constexpr int kGroupedStages = 6;
-constexpr int kGroupedSmem = kGroupedStages * kGroupedStage + 4 * kEpiWarpBytes + 1024;
+// Ring of (A half, B half): six steps of 256-row tiles, or nine of tiles of at
+// most 64 rows, whose B half is a quarter: where groups are that small reading
+// the matrices is the cost, and three more steps in flight cover HBM's latency.
+constexpr int grouped_stage(bool small) { return kHalfTile + (small ? kHalfTile / 4 : kHalfTile); }
+constexpr int grouped_stages(bool small) { return small ? 9 : 6; }
+constexpr int grouped_smem(bool small) { return grouped_stages(small) * grouped_stage(small) + 4 * kEpiWarpBytes + 1024; }
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
 // 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
@@ -54,7 +57,7 @@ constexpr int kGroupedMaxGroups = 1024;
 // many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
 // by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
 constexpr int kPartSteps = 8;
-static_assert(kGroupedSmem + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
+static_assert(grouped_smem(false) + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
 
 struct GroupedMaps {
     CUtensorMap a, b, c;  // c: forward and rows, b in 32-row boxes; weights, the result
@@ -190,11 +193,12 @@ MOE_DEV int adapter_of(const AdapterArgs& p, int t) {
     return id >= 0 && id < p.L ? id : -1;
 }
 
-template <int MODE, bool OUT32, bool ADAPT>
+template <int MODE, bool OUT32, bool ADAPT, bool SMALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     grouped_kernel(const GroupedArgs g, const __grid_constant__ GroupedExtra<ADAPT> ex, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap) {
     constexpr bool WG = MODE == kGroupedWeights;
+    constexpr int kGroupedStage = grouped_stage(SMALL), kGroupedStages = grouped_stages(SMALL);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[kGroupedStages], empty_bar[kGroupedStages], tail_bar[kGroupedStages];
     __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
@@ -700,6 +704,14 @@ static int sm_count() {
     return sms;
 }
 
+// Rows per block: 256, less where that leaves SMs without a tile (a matrix read
+// by more blocks comes from L2).
+static int block_limit(int rows, int features) {
+    const int64_t JT = (features + 255) / 256, pairs = sm_count() / 2;
+    const int64_t even = (rows * JT / pairs + 31) / 32 * 32;
+    return (int)(even < 32 ? 32 : even > 256 ? 256 : even);
+}
+
 // map of a row-major 16-bit matrix [rows x cols], rows `ld` values apart; boxes of 64 columns x box_rows
 static Elem elem16(bool bf16) { return bf16 ? Elem::kBf16 : Elem::kFp16; }
 static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld,
@@ -709,18 +721,10 @@ static cudaError_t map_2d(CUtensorMap* m, bool bf16, const void* base, int64_t r
     return encode_tiles(m, elem16(bf16), base, 2, dims, str, box, 128);
 }
 
-// Rows per block: 256, less where that leaves SMs without a tile (a matrix read
-// by more blocks comes from L2).
-static int block_limit(int rows, int features) {
-    const int64_t JT = (features + 255) / 256, pairs = sm_count() / 2;
-    const int64_t even = (rows * JT / pairs + 31) / 32 * 32;
-    return (int)(even < 32 ? 32 : even > 256 ? 256 : even);
-}
-
-template <int MODE, bool OUT32>
+template <int MODE, bool OUT32, bool SMALL>
 static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, int64_t most_tiles, cudaStream_t s) {
-    auto kern = grouped_kernel<MODE, OUT32, false>;
-    constexpr int smem = kGroupedSmem;
+    auto kern = grouped_kernel<MODE, OUT32, false, SMALL>;
+    constexpr int smem = grouped_smem(SMALL);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
@@ -740,7 +744,7 @@ static cudaError_t product_maps(GroupedMaps* m, bool forward, bool bf, int E, in
     return e;
 }
 
-template <bool OUT32>
+template <bool OUT32, bool SMALL>
 static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t s) {
     GroupedMaps m;
     cudaError_t e = product_maps(&m, true, bf16, 1, p.N, p.K, p.w, p.x, p.T, p.ldx);
@@ -769,8 +773,8 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
         if (e == cudaSuccess) e = encode_tiles(&ex.v_small, elem16(bf16), p.v, 3, vd, vs, small, 128);
         if (e != cudaSuccess) return e;
     }
-    auto kern = grouped_kernel<kGroupedForward, OUT32, true>;
-    constexpr int smem = kGroupedSmem;
+    auto kern = grouped_kernel<kGroupedForward, OUT32, true, SMALL>;
+    constexpr int smem = grouped_smem(SMALL);
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // (runs cut blocks off: at most one block more per run of 32 tokens)
@@ -789,7 +793,9 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
 }
 
 cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {
-    return out32 ? adapter_launch<true>(p, bf16, s) : adapter_launch<false>(p, bf16, s);
+    if (block_limit(p.T, p.N) <= 64)
+        return out32 ? adapter_launch<true, true>(p, bf16, s) : adapter_launch<false, true>(p, bf16, s);
+    return out32 ? adapter_launch<true, false>(p, bf16, s) : adapter_launch<false, false>(p, bf16, s);
 }
 
 cudaError_t launch_grouped(int mode, const GroupedArgs& args, const void* w, const void* x, int64_t ldx, const void* dy,
@@ -810,8 +816,8 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& args, const void* w, con
         if (e == cudaSuccess) e = encode_tiles(&m.c, out_fp32 ? Elem::kFp32 : elem16(bf), g.out, 3, dims, str, box, 64);
         if (e != cudaSuccess) return e;
         const int64_t tiles = (int64_t)g.E * JT * ((g.C + 255) / 256);
-        return out_fp32 ? grouped_launch<kGroupedWeights, true>(g, m, tiles, s)
-                        : grouped_launch<kGroupedWeights, false>(g, m, tiles, s);
+        return out_fp32 ? grouped_launch<kGroupedWeights, true, false>(g, m, tiles, s)
+                        : grouped_launch<kGroupedWeights, false, false>(g, m, tiles, s);
     }
     const bool forward = mode == kGroupedForward;
     if (forward && g.M <= kSkinnyMaxRows) return launch_skinny_grouped(g, w, x, ldx, out_fp32, s);
@@ -819,11 +825,17 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& args, const void* w, con
                      forward ? ldx : lddy);
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((int64_t)(g.M + g.block - 1) / g.block + (g.E < g.M ? g.E : g.M)) * JT;
-    if (mode == kGroupedForward)
-        return out_fp32 ? grouped_launch<kGroupedForward, true>(g, m, tiles, s)
-                        : grouped_launch<kGroupedForward, false>(g, m, tiles, s);
-    return out_fp32 ? grouped_launch<kGroupedRows, true>(g, m, tiles, s)
-                    : grouped_launch<kGroupedRows, false>(g, m, tiles, s);
+    const bool small = g.block <= 64;
+    if (forward) {
+        if (small) return out_fp32 ? grouped_launch<kGroupedForward, true, true>(g, m, tiles, s)
+                                   : grouped_launch<kGroupedForward, false, true>(g, m, tiles, s);
+        return out_fp32 ? grouped_launch<kGroupedForward, true, false>(g, m, tiles, s)
+                        : grouped_launch<kGroupedForward, false, false>(g, m, tiles, s);
+    }
+    if (small) return out_fp32 ? grouped_launch<kGroupedRows, true, true>(g, m, tiles, s)
+                               : grouped_launch<kGroupedRows, false, true>(g, m, tiles, s);
+    return out_fp32 ? grouped_launch<kGroupedRows, true, false>(g, m, tiles, s)
+                    : grouped_launch<kGroupedRows, false, false>(g, m, tiles, s);
 }
 
 }  // namespace moe

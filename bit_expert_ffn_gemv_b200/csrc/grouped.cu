@@ -43,7 +43,8 @@ namespace moe {
 constexpr int kGroupedThreads = 256;
 constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an operand, one K = 64 step
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
-constexpr int kEpiWarpBytes = 4096;             // epilogue transpose buffer of one warp
+constexpr int kRowPitch = 36;                   // floats: fp32 rows of 32 features, padded
+constexpr int kEpiWarpBytes = 2 * 16 * kRowPitch * 4;  // epilogue transpose buffers of one warp
 // Ring of (A half, B half): six steps of 256-row tiles, or nine of tiles of at
 // most 64 rows, whose B half is a quarter: where groups are that small reading
 // the matrices is the cost, and three more steps in flight cover HBM's latency.
@@ -75,9 +76,6 @@ MOE_DEV uint32_t pack16(float lo, float hi, bool bf16) {
 MOE_DEV uint16_t to16(float v, bool bf16) {
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
-
-// *p += v without waiting for the old value (one thread owns p: its additions keep their order)
-MOE_DEV void add_global(float* p, float v) { asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
 
 struct GroupedTile {
     int e, row0, n;  // group; first row and rows of the tile (weights: of the group)
@@ -149,26 +147,27 @@ MOE_DEV GroupedTile tile_at(const GroupedArgs& g, int t, const TileList& l, int 
 // fall along the list every pair gets about the same sum.
 MOE_DEV int tile_index(int i, int p, int P) { return i * P + ((i & 1) ? P - 1 - p : p); }
 
-// Exclusive scan (sum, or running maximum from `start`) of one value per thread
-// over the CTA; every thread calls it.
-template <bool MAX>
-MOE_DEV int block_exclusive(int v, int start, int* wsum) {
+// Exclusive prefix sum of one value per thread over the CTA, and the total;
+// every thread calls it.
+MOE_DEV int block_exclusive(int v, int* wsum, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc = MAX ? max(inc, u) : inc + u;
+        if (lane >= o) inc += u;
     }
-    int ex = __shfl_up_sync(0xffffffffu, inc, 1);
-    if (lane == 0) ex = start;
-    __syncthreads();  // (an earlier scan's sums have been read)
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
+    int before = inc - v;
+    total = 0;
 #pragma unroll
-    for (int w = 0; w < kGroupedThreads / 32; ++w)
-        if (w < warp) ex = MAX ? max(ex, wsum[w]) : ex + wsum[w];
-    return ex;
+    for (int w = 0; w < kGroupedThreads / 32; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+    }
+    __syncthreads();  // (wsum may be written again)
+    return before;
 }
 
 // Adapters (one "group" per run of tokens of one adapter, below): the maps of B
@@ -223,8 +222,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tc::tmem_alloc_pair(&tmem_slot, 512);
+    if (warp == 3 && lane < 3) tc::prefetch_map(lane == 0 ? &amap : lane == 1 ? &bmap : &cmap);
 
-    constexpr int kPer = kGroupedMaxGroups / kGroupedThreads;
+    // (the loops below stay rolled: this part runs once, and its instructions come from memory)
     int E = g.E;
     bool runs = false;  // adapters: every tile has one adapter
     if constexpr (ADAPT) {
@@ -241,10 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             n += id != was;
             was = id;
         }
-        int at = block_exclusive<false>(n, 0, wsum);
-        if (tid == kGroupedThreads - 1) pre[0] = at + n;
-        __syncthreads();
-        const int found = pre[0];
+        int found;
+        int at = block_exclusive(n, wsum, found);
         runs = found <= kGroupedMaxGroups && (int64_t)found * 32 <= g.M;
         E = runs ? found : 1;
         if (runs) {
@@ -260,27 +258,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             start[E] = g.M;
         }
     } else {
-        // Group starts: clamped into [0, rows] and made ascending by a running
-        // maximum, so that a bad table reads and writes nothing out of range.
-        const int first = min(max(__ldg(&g.offsets[0]), 0), g.M);
-        int end[kPer], top = first;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = tid * kPer + i;
-            if (e < E) top = max(top, min(max(__ldg(&g.offsets[e + 1]), 0), g.M));
-            end[i] = top;
+        // Group starts: clamped into [0, rows] and made ascending, so that a bad
+        // table reads and writes nothing out of range.
+        bool rising = true;
+#pragma unroll 1
+        for (int e = tid; e < E; e += kGroupedThreads) {
+            const int a = min(max(__ldg(&g.offsets[e]), 0), g.M), b = min(max(__ldg(&g.offsets[e + 1]), 0), g.M);
+            start[e] = a;
+            if (e == E - 1) start[E] = b;
+            rising = rising && a <= b;
         }
-        const int top_before = block_exclusive<true>(top, first, wsum);
-        int begin = max(top_before, first);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = tid * kPer + i, stop = max(end[i], begin);
-            if (e < E) {
-                start[e] = begin;
-                order[e] = WG ? stop - begin : block_rows(stop - begin, g.block);  // the sort key: rows of one tile
-            }
-            if (e == E - 1) start[E] = stop;
-            begin = stop;
+        if (!__syncthreads_and(rising)) {
+            if (tid == 0)
+                for (int e = 0; e < E; ++e) start[e + 1] = max(start[e + 1], start[e]);
         }
     }
     __syncthreads();
@@ -288,49 +278,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     // pairs end together.  Where the groups are so small that reading their
     // matrices is the cost (under 256 rows on average), the groups' own order,
     // which mixes short and long tiles and keeps HBM busy throughout.
-    int place[kPer];
     const bool sorted = !ADAPT && (WG || start[E] - start[0] >= 256 * E);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        place[i] = e;
-        if (sorted && e < E) {
-            const int key = order[e];
+    if (sorted) {
+        auto key = [&](int e) {
+            const int c = start[e + 1] - start[e];
+            return WG ? c : block_rows(c, g.block);
+        };
+#pragma unroll 1
+        for (int e = tid; e < E; e += kGroupedThreads) {
+            const int mine = key(e);
             int n = 0;
+#pragma unroll 1
             for (int o = 0; o < E; ++o) {
-                const int k = order[o];
-                n += k > key || (k == key && o < e);
+                const int k = key(o);
+                n += k > mine || (k == mine && o < e);
             }
-            place[i] = n;
+            order[n] = e;
         }
+    } else {
+#pragma unroll 1
+        for (int e = tid; e < E; e += kGroupedThreads) order[e] = e;
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (tid * kPer + i < E) order[place[i]] = tid * kPer + i;
     __syncthreads();
     int total;
     if (WG) {
         total = E * JT * ((g.C + 255) >> 8);
     } else {
-        int mine = 0, blocks[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = tid * kPer + i;
-            const int e = at < E ? order[at] : 0;
-            blocks[i] = at < E ? block_count(start[e + 1] - start[e], g.block) : 0;
-            mine += blocks[i];
+        int all = 0;
+#pragma unroll 1
+        for (int base = 0; base < E; base += kGroupedThreads) {
+            const int at = base + tid, e = at < E ? order[at] : 0;
+            int sum;
+            const int before = block_exclusive(at < E ? block_count(start[e + 1] - start[e], g.block) : 0, wsum, sum);
+            if (at < E) pre[at] = all + before;
+            all += sum;
         }
-        int before = block_exclusive<false>(mine, 0, wsum);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = tid * kPer + i;
-            if (at < E) pre[at] = before;
-            before += blocks[i];
-            if (at == E - 1) pre[E] = before;
-        }
-        __syncthreads();
-        total = pre[E] * JT;
+        if (tid == 0) pre[E] = all;
+        total = all * JT;
     }
     const TileList list{start, pre, order, E};
     tc::fence_before();
@@ -540,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     // 32 rows at a time.  TMEM is read as warp-MMA fragments, so an adapter's delta is added in
                     // registers; 16-bit results are packed in pairs and transposed by stmatrix into [row][32
                     // features] (16-byte pieces permuted against bank conflicts), then leave as whole pieces of
-                    // the rows.  fp32 results leave from the fragments: 8 lanes fill a 32-byte sector
+                    // the rows
                     const int seg = lane & 3, vr = lane >> 2;
                     const bool in = f + seg * 8 < g.F;
                     const int64_t at = (int64_t)tl.row0 * g.ldo + f;
@@ -578,19 +562,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         }
                         const bool more = c0 + 32 < tl.n;
                         if (OUT32) {
-                            float* out = static_cast<float*>(g.out) + at + (int64_t)c0 * g.ldo;
+                            // 16 rows at a time through two buffers (rows of 32 features, padded against bank
+                            // conflicts); lane l sends row l.  Later parts are added in L2 by the copy itself,
+                            // each part once the one before has landed: a fixed order of additions
+                            if (part > 0 && c0 == 0) tc::store_wait_done();
 #pragma unroll
-                            for (int m = 0; m < 2; ++m)
+                            for (int h = 0; h < 2; ++h) {
+                                if (c0 + 16 * h >= tl.n) break;
+                                float* buf = reinterpret_cast<float*>(stg) + h * 16 * kRowPitch;
+                                tc::store_wait_read<1>();
+                                __syncwarp();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const int row = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
-                                    const int ff = 16 * m + (lane >> 2) + 8 * ((i >> 1) & 1);
-                                    if (c0 + row < tl.n && f + ff < g.F) {
-                                        float* p = out + (int64_t)row * g.ldo + ff;
-                                        if (add) add_global(p, __uint_as_float(r[m][i]));
-                                        else *p = __uint_as_float(r[m][i]);
-                                    }
+                                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        buf[(8 * (i >> 2) + 2 * (lane & 3) + (i & 1)) * kRowPitch + 16 * m + (lane >> 2) +
+                                            8 * ((i >> 1) & 1)] = __uint_as_float(r[m][8 * h + i]);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                                const int row = c0 + 16 * h + lane;
+                                if (lane < 16 && row < tl.n && f < g.F) {
+                                    float* dst = static_cast<float*>(g.out) + at + (int64_t)row * g.ldo;
+                                    const uint32_t bytes = (uint32_t)min(32, g.F - f) * 4u;
+                                    if (add) tc::bulk_add(dst, buf + lane * kRowPitch, bytes);
+                                    else tc::bulk_store(dst, buf + lane * kRowPitch, bytes);
                                 }
+                                tc::store_commit();
+                            }
                             if (more) {
                                 tc::ld_frags_nowait(tb + c0 + 32, r[0]);
                                 tc::ld_frags_nowait(tb + (16u << 16) + c0 + 32, r[1]);
@@ -682,11 +680,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 if (!empty) {
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&acce_bar[b], 0));
+                    // (relaxed: the accumulator has been read into registers, and the release of the
+                    // stores above, which no one waits for here, would take ~700 cycles)
+                    if (lane == 0) tc::arrive_cluster_relaxed(tc::cluster_addr(&acce_bar[b], 0));
                 }
             }
         }
-        if (WG && one) tc::store_wait_done();
+        if ((WG && one) || (!WG && OUT32)) tc::store_wait_done();
         if (!ok) tc::settle();
     }
     tc::fence_before();

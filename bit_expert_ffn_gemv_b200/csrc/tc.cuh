@@ -151,6 +151,9 @@ MOE_DEV void arrive_cluster(uint32_t bar, uint32_t count = 1) {
 }
 // (relaxed: announces a copy's bytes, publishes no memory of this thread; a
 // release here drains the thread's outstanding operations, ~0.7 us per step)
+MOE_DEV void arrive_cluster_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 MOE_DEV void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
@@ -210,11 +213,17 @@ MOE_DEV void tma_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z,
         : "memory");
 }
 
-// fetch a tile into L2
-MOE_DEV void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z)
+MOE_DEV void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// untiled copies of `bytes` (a multiple of 16, both addresses 16-byte aligned)
+MOE_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+MOE_DEV void bulk_add(float* dst, const float* src, uint32_t bytes) {
+    asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst),
+                 "r"(smem_addr(src)), "r"(bytes)
                  : "memory");
 }
 // TMA tile stores from this CTA's shared memory (bulk groups of the issuing thread)

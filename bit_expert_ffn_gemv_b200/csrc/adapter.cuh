@@ -1,5 +1,5 @@
-// adapter.cuh -- the inner values v of the tokens' adapters and their delta
-// B_a v_t, as warp-MMA fragments of 32 features by 16 tokens.
+// adapter.cuh -- the inner values v of the tokens' adapters as 16-bit terms, and
+// their delta B_a v_t in warp-MMA fragments.
 //
 // v is fp32; the MMA takes 16-bit operands, so v is split into terms of B's
 // type (v = hi + lo [+ lower], each exact in what the ones before leave): two
@@ -33,95 +33,101 @@ MOE_DEV uint16_t take_term(float& v) {
     return t;
 }
 
-// d[m][n][i]: feature 16 m + lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2
-struct DeltaFrags {
-    float d[2][2][4];
-};
-MOE_DEV int frag_feature(int m, int i) { return 16 * m + ((threadIdx.x & 31) >> 2) + 8 * (i >> 1); }
-MOE_DEV int frag_token(int n, int i) { return 8 * n + 2 * (threadIdx.x & 3) + (i & 1); }
-
-// Frags of B_a[f0 .. f0 + 31] . v of tokens t0 .. t0 + 15 that are in `used`
-// (a bit per token; the others' columns hold nothing meaningful).  Lane l / 4
-// reads token l / 4 (+ 8) and feature rows l / 4 + 8 i; lane l % 4 takes four
+// Adds the delta of tokens t0 .. t0 + n - 1 (n <= 16) to MMA fragments of fp32
+// bits: lo[4 q + i] is feature f0 + lane / 4 + 8 (i / 2), token 8 q + 2 (lane %
+// 4) + i % 2; hi the same 16 features further.  Whole warps, any order of ids.
+//
+// 32 rank values at a time: v's fragments of all 16 tokens are loaded once, then
+// each distinct adapter among them takes one pass of MMAs whose columns are kept
+// for its own tokens only (another adapter's infinities must not reach a token).
+// The next adapter's rows of B load behind the pass, and those of the tokens
+// after these (next .. next + n_next - 1) are fetched into L1.  Lane l / 4 reads
+// token l / 4 (+ 8) and feature rows l / 4 + 8 i; lane l % 4 takes four
 // consecutive rank values of each, the same for both operands.
 template <bool BF16, int TERMS>
-MOE_DEV void adapter_delta(const AdapterArgs& p, int t0, uint32_t used, int a, int f0, DeltaFrags& out) {
+MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next, int f0, uint32_t* lo, uint32_t* hi) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out.d[m][n][i] = 0.f;
-    const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)a * p.N) * p.r;
-    const uint16_t* row[4];  // features f0 + gq + 8 i (past N: any row, its results are not stored)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) row[i] = B + (int64_t)min(f0 + gq + 8 * i, p.N - 1) * p.r;
-    const int quads = p.r >> 2;
-    const bool use[2] = {((used >> gq) & 1) != 0, ((used >> (8 + gq)) & 1) != 0};
-    const int64_t vrow = (int64_t)(t0 + gq) * p.r;
-#pragma unroll 4
-    for (int q0 = 0; q0 < quads; q0 += 4) {
-        const int q = q0 + c;
-        uint2 w[4], v[2][TERMS];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = q < quads ? __ldg(reinterpret_cast<const uint2*>(row[i] + 4 * q)) : make_uint2(0, 0);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int k = 0; k < TERMS; ++k) {
-                v[n][k] = make_uint2(0, 0);
-                if (q < quads && use[n])
-                    v[n][k] = *reinterpret_cast<const uint2*>(adapter_term(p, k) + vrow + (int64_t)n * 8 * p.r + 4 * q);
-            }
-        const uint32_t f0r[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, f1r[4] = {w[2].x, w[3].x, w[2].y, w[3].y};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int k = 0; k < TERMS; ++k) {
-                mma16<BF16>(out.d[0][n], f0r, v[n][k].x, v[n][k].y);
-                mma16<BF16>(out.d[1][n], f1r, v[n][k].x, v[n][k].y);
-            }
-    }
-    if (!BF16) {
-        const float* back = adapter_back(p, TERMS) + t0;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 8 * n + 2 * c + i;
-                const float s = (used >> t) & 1 ? back[t] : 1.f;
-                out.d[0][n][i] *= s, out.d[0][n][i + 2] *= s, out.d[1][n][i] *= s, out.d[1][n][i + 2] *= s;
-            }
-    }
-}
-
-// Adds the delta of tokens t0 .. t0 + n - 1 (n <= 16) to the fragments lo
-// (features f0 .. f0 + 15) and hi (f0 + 16 .. f0 + 31): two of 8 tokens each,
-// fp32 bits.  Whole warps; any order of ids, one pass per distinct adapter.
-template <bool BF16, int TERMS>
-MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int f0, uint32_t* lo, uint32_t* hi) {
-    const int lane = threadIdx.x & 31;
     int id = lane < n ? __ldg(&p.ids[t0 + lane]) : -1;
+    int id_next = lane < n_next ? __ldg(&p.ids[next + lane]) : -1;
     if (id < 0 || id >= p.L) id = -1;
-    const uint32_t mine = __match_any_sync(0xffffffffu, id);
-    uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
-    while (todo) {
-        const int leader = __ffs(todo) - 1;
-        const int a = __shfl_sync(0xffffffffu, id, leader);
-        const uint32_t used = __shfl_sync(0xffffffffu, mine, leader);
-        todo &= ~used;
-        DeltaFrags fr;
-        adapter_delta<BF16, TERMS>(p, t0, used, a, f0, fr);
+    if (id_next < 0 || id_next >= p.L) id_next = -1;
+    const uint16_t* B = static_cast<const uint16_t*>(p.b);
+    const int quads = p.r >> 2;
+    const uint32_t mine = __match_any_sync(0xffffffffu, id), mine_next = __match_any_sync(0xffffffffu, id_next);
+    if (id_next >= 0 && (mine_next & ((1u << lane) - 1)) == 0) {  // an adapter's first token: its 32 rows are contiguous
+        const char* rows = reinterpret_cast<const char*>(B + ((int64_t)id_next * p.N + f0) * p.r);
+        for (int i = 0; i < 64 * min(p.r, 64) && f0 + 32 <= p.N; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + i));
+    }
+    const uint32_t all = __ballot_sync(0xffffffffu, id >= 0);
+    if (!all) return;
+    const bool use[2] = {((all >> gq) & 1) != 0, ((all >> (8 + gq)) & 1) != 0};
+    float back[4];  // fp16: undoes the scale of tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+    for (int i = 0; i < 4; ++i) {
+        const int t = 8 * (i >> 1) + 2 * c + (i & 1);
+        back[i] = !BF16 && ((all >> t) & 1) ? adapter_back(p, TERMS)[t0 + t] : 1.f;
+    }
+    int64_t at[4];  // offset of feature rows f0 + gq + 8 i in one adapter's B (past N: any row, not stored)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // (another adapter's infinities must not reach this token)
-                if (!((used >> frag_token(q, i)) & 1)) continue;
-                lo[4 * q + i] = __float_as_uint(__uint_as_float(lo[4 * q + i]) + fr.d[0][q][i]);
-                hi[4 * q + i] = __float_as_uint(__uint_as_float(hi[4 * q + i]) + fr.d[1][q][i]);
+    for (int i = 0; i < 4; ++i) at[i] = (int64_t)min(f0 + gq + 8 * i, p.N - 1) * p.r + 4 * c;
+    for (int j0 = 0; j0 < p.r; j0 += 32) {
+        uint2 v[2][2][TERMS], w[2][4], w_next[2][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k) {
+                    v[s][q][k] = make_uint2(0, 0);
+                    if (j0 + 16 * s + 4 * c < p.r && use[q])
+                        v[s][q][k] = *reinterpret_cast<const uint2*>(adapter_term(p, k) + (int64_t)(t0 + gq + 8 * q) * p.r + j0 +
+                                                                     16 * s + 4 * c);
+                }
+        auto load = [&](int a, uint2 (&to)[2][4]) {
+            const uint16_t* rows = B + (int64_t)a * p.N * p.r + j0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    to[s][i] = j0 + 16 * s + 4 * c < p.r ? __ldg(reinterpret_cast<const uint2*>(rows + at[i] + 16 * s)) : make_uint2(0, 0);
+        };
+        uint32_t todo = all;
+        int leader = __ffs(todo) - 1;
+        load(__shfl_sync(0xffffffffu, id, leader), w);
+        while (todo) {
+            const uint32_t used = __shfl_sync(0xffffffffu, mine, leader);
+            todo &= ~used;
+            if (todo) {
+                leader = __ffs(todo) - 1;
+                load(__shfl_sync(0xffffffffu, id, leader), w_next);
             }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!((used >> (8 * q)) & 0xffu)) continue;
+                float d[2][4] = {};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t fa[4] = {w[s][0].x, w[s][1].x, w[s][0].y, w[s][1].y};
+                    const uint32_t fb[4] = {w[s][2].x, w[s][3].x, w[s][2].y, w[s][3].y};
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) {
+                        mma16<BF16>(d[0], fa, v[s][q][k].x, v[s][q][k].y);
+                        mma16<BF16>(d[1], fb, v[s][q][k].x, v[s][q][k].y);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!((used >> (8 * q + 2 * c + (i & 1))) & 1)) continue;
+                    const float s = back[2 * q + (i & 1)];
+                    lo[4 * q + i] = __float_as_uint(BF16 ? __uint_as_float(lo[4 * q + i]) + d[0][i] : fmaf(d[0][i], s, __uint_as_float(lo[4 * q + i])));
+                    hi[4 * q + i] = __float_as_uint(BF16 ? __uint_as_float(hi[4 * q + i]) + d[1][i] : fmaf(d[1][i], s, __uint_as_float(hi[4 * q + i])));
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[s][i] = w_next[s][i];
+        }
     }
 }
 

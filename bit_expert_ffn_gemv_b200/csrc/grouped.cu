@@ -540,9 +540,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
                                     if (c0 + 16 * h < tl.n) {
-                                        const int m = min(16, tl.n - c0 - 16 * h);
-                                        if (bf16) add_delta<true, kTerms>(ex.args, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
-                                        else add_delta<false, 2>(ex.args, tl.row0 + c0 + 16 * h, m, f, &r[0][8 * h], &r[1][8 * h]);
+                                        const int t0 = tl.row0 + c0 + 16 * h, left = tl.n - c0 - 16 * h;
+                                        const int m = min(16, left), mn = min(16, left - 16);
+                                        if (bf16) add_delta<true, kTerms>(ex.args, t0, m, t0 + 16, mn, f, &r[0][8 * h], &r[1][8 * h]);
+                                        else add_delta<false, 2>(ex.args, t0, m, t0 + 16, mn, f, &r[0][8 * h], &r[1][8 * h]);
                                     }
                         }
                         if (ADAPT && !OUT32 && g.accumulate) {  // y's values, added before the one rounding
@@ -563,31 +564,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         const bool more = c0 + 32 < tl.n;
                         if (OUT32) {
                             // 16 rows at a time through two buffers (rows of 32 features, padded against bank
-                            // conflicts); lane l sends row l.  Later parts are added in L2 by the copy itself,
-                            // each part once the one before has landed: a fixed order of additions
-                            if (part > 0 && c0 == 0) tc::store_wait_done();
+                            // conflicts), 16 bytes a lane.  Later parts are added in L2, no old value is waited
+                            // for: one lane owns an address, so its additions keep their order
+                            const int fr = lane >> 3, fs = (lane & 7) * 4;
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 if (c0 + 16 * h >= tl.n) break;
                                 float* buf = reinterpret_cast<float*>(stg) + h * 16 * kRowPitch;
-                                tc::store_wait_read<1>();
-                                __syncwarp();
 #pragma unroll
                                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                                     for (int i = 0; i < 8; ++i)
                                         buf[(8 * (i >> 2) + 2 * (lane & 3) + (i & 1)) * kRowPitch + 16 * m + (lane >> 2) +
                                             8 * ((i >> 1) & 1)] = __uint_as_float(r[m][8 * h + i]);
-                                fence_proxy_async_smem();
                                 __syncwarp();
-                                const int row = c0 + 16 * h + lane;
-                                if (lane < 16 && row < tl.n && f < g.F) {
-                                    float* dst = static_cast<float*>(g.out) + at + (int64_t)row * g.ldo;
-                                    const uint32_t bytes = (uint32_t)min(32, g.F - f) * 4u;
-                                    if (add) tc::bulk_add(dst, buf + lane * kRowPitch, bytes);
-                                    else tc::bulk_store(dst, buf + lane * kRowPitch, bytes);
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4) {
+                                    const int row = c0 + 16 * h + 4 * q4 + fr;
+                                    if (row < tl.n && f + fs < g.F) {
+                                        const float4 v = *reinterpret_cast<const float4*>(buf + (4 * q4 + fr) * kRowPitch + fs);
+                                        float* dst = static_cast<float*>(g.out) + at + (int64_t)row * g.ldo + fs;
+                                        if (add) tc::add_global4(dst, v);
+                                        else *reinterpret_cast<float4*>(dst) = v;
+                                    }
                                 }
-                                tc::store_commit();
                             }
                             if (more) {
                                 tc::ld_frags_nowait(tb + c0 + 32, r[0]);
@@ -686,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 }
             }
         }
-        if ((WG && one) || (!WG && OUT32)) tc::store_wait_done();
+        if (WG && one) tc::store_wait_done();
         if (!ok) tc::settle();
     }
     tc::fence_before();

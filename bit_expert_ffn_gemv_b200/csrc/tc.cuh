@@ -216,15 +216,9 @@ MOE_DEV void tma_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z,
 MOE_DEV void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// untiled copies of `bytes` (a multiple of 16, both addresses 16-byte aligned)
-MOE_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
-                 : "memory");
-}
-MOE_DEV void bulk_add(float* dst, const float* src, uint32_t bytes) {
-    asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst),
-                 "r"(smem_addr(src)), "r"(bytes)
-                 : "memory");
+// p[0..3] += v, without waiting for the old values
+MOE_DEV void add_global4(float* p, float4 v) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 // TMA tile stores from this CTA's shared memory (bulk groups of the issuing thread)
 MOE_DEV void store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {

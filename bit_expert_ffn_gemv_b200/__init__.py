@@ -323,6 +323,29 @@ class MoeLayer:
         moe_forward(self.handle, layer, x.data_ptr(), T, y.data_ptr(), flags, _stream_ptr(stream))
         return y
 
+    def forward_adapted(self, layer, x, a, b, ids, scale=None, y=None, flags=0, stream=None):
+        """The layer with each token's low-rank adapter beside it: y = [y +] layer(u) + scale[i] b[i] a[i] u with
+        u = x, or rmsnorm(x) with MOE_NORM_INPUT, and i = ids[t] (outside [0, L): no adapter).
+
+        a [L, rank, d] and b [L, d, rank] bf16, ids int32 [T], scale fp32 [L] as in adapter_project.  The adapters'
+        term is added to the layer's result: a bf16 y is rounded by the layer and again by the sum, an fp32 y
+        (MOE_OUT_FP32) not at all.  y == x (a residual update in place) needs MOE_NORM_INPUT, whose normalised copy
+        the adapters read.  With a handle restricted to an expert range, add the adapters on one rank only.
+        """
+        import torch
+        from .experts16 import adapter_project
+        if y is not None and y.data_ptr() == x.data_ptr() and not flags & MOE_NORM_INPUT:
+            raise ValueError("y == x: the adapters read x after the layer has updated it (use MOE_NORM_INPUT)")
+        u = x
+        if flags & MOE_NORM_INPUT:
+            with torch.cuda.device(x.device):
+                u = rms_normalize(x, stream=stream)
+            if stream is not None:
+                u.record_stream(stream)  # freed on return, possibly before the calls below have run
+        y = self.forward(layer, u, y, flags & ~MOE_NORM_INPUT, stream)
+        return adapter_project(u, a, b, ids, scale=scale, out=y, flags=MOE_ACCUMULATE | (flags & MOE_OUT_FP32),
+                               stream=stream)
+
     def forward_host(self, layer, x_host, y_host, flags=0, stream=None):
         moe_forward_host(self.handle, layer, x_host.data_ptr(), x_host.shape[0], y_host.data_ptr(), flags,
                          _stream_ptr(stream))

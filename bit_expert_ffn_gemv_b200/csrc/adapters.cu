@@ -34,16 +34,18 @@ namespace moe {
 // chunk.
 constexpr int kShrinkThreads = 256;
 
-// rank values per pass and octets of tokens per item: the accumulators stay in registers
-template <int WIN>
+// Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K
+// whose operands are in registers at once: as many as 64 to 72 registers hold.
+template <int WIN, int TILES>
 struct ShrinkCfg {
-    static constexpr int kOctets = WIN / 8, kRows = WIN == 8 ? 64 : 32, kTiles = kRows / 16, kPitch = kRows + 4;
+    static constexpr int kOctets = WIN / 8, kTiles = TILES, kRows = 16 * TILES, kPitch = kRows + 4;
+    static constexpr int kVecs = kOctets + 2 * TILES, kSteps = 4 * kVecs <= 18 ? 4 : 3 * kVecs <= 18 ? 3 : 2;
     static constexpr int kRed = 8 * WIN * kPitch * 4;  // bytes: [warp][token of its item][row]
 };
 
-template <bool BF16, int WIN, int TERMS>
+template <bool BF16, int WIN, int TERMS, int TILES>
 __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const AdapterArgs p) {
-    using C = ShrinkCfg<WIN>;
+    using C = ShrinkCfg<WIN, TILES>;
     extern __shared__ __align__(16) uint8_t shrink_smem[];
     float* red = reinterpret_cast<float*>(shrink_smem);                 // [8][WIN][kPitch]
     float* sums = reinterpret_cast<float*>(shrink_smem + C::kRed);      // [WIN][r]
@@ -93,22 +95,21 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
 #pragma unroll
                 for (int q = 0; q < 2 * C::kTiles; ++q)
                     ar[q] = A + ((int64_t)a * p.r + j0 + (q * 8 + gq < rows ? q * 8 + gq : gq)) * p.K + 8 * c;
-                // a step's operands load while the step before is multiplied; only a last, partial
-                // step looks at the end of K
-                uint4 bv[2][C::kOctets], av[2][2 * C::kTiles];
+                // a step's operands load kSteps - 1 steps before it is multiplied; only a last, partial step
+                // looks at the end of K
+                uint4 bv[C::kSteps][C::kOctets], av[C::kSteps][2 * C::kTiles];
                 auto load = [&](int b, int k) {
                     if (k + 32 <= ke) {
 #pragma unroll
                         for (int o = 0; o < C::kOctets; ++o) bv[b][o] = __ldg(reinterpret_cast<const uint4*>(xr[o] + k));
 #pragma unroll
-                        for (int q = 0; q < 2 * C::kTiles; ++q)
-                            if (q < 2 * tiles) av[b][q] = __ldg(reinterpret_cast<const uint4*>(ar[q] + k));
+                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = __ldg(reinterpret_cast<const uint4*>(ar[q] + k));
                     } else {
                         const bool in = k + 8 * c < ke;
 #pragma unroll
                         for (int o = 0; o < C::kOctets; ++o) bv[b][o] = load_or_zero(xr[o] + k, in);
 #pragma unroll
-                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = load_or_zero(ar[q] + k, in && q < 2 * tiles);
+                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = load_or_zero(ar[q] + k, in);
                     }
                 };
                 auto multiply = [&](int b) {
@@ -116,21 +117,24 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                     for (int q = 0; q < C::kTiles; ++q) {
                         const uint4 lo = av[b][2 * q], hi = av[b][2 * q + 1];
                         const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
-                        if (q < tiles) {
 #pragma unroll
-                            for (int o = 0; o < C::kOctets; ++o) {
-                                mma16<BF16>(acc[q][o], f0, bv[b][o].x, bv[b][o].y);
-                                mma16<BF16>(acc[q][o], f1, bv[b][o].z, bv[b][o].w);
-                            }
+                        for (int o = 0; o < C::kOctets; ++o) {
+                            if (o > 0 && octets == 1) break;
+                            mma16<BF16>(acc[q][o], f0, bv[b][o].x, bv[b][o].y);
+                            mma16<BF16>(acc[q][o], f1, bv[b][o].z, bv[b][o].w);
                         }
                     }
                 };
-                load(0, kb);
-                for (int k0 = kb; k0 < ke; k0 += 64) {
-                    if (k0 + 32 < ke) load(1, k0 + 32);
-                    multiply(0);
-                    if (k0 + 64 < ke) load(0, k0 + 64);
-                    if (k0 + 32 < ke) multiply(1);
+#pragma unroll
+                for (int b = 0; b < C::kSteps - 1; ++b)
+                    if (kb + 32 * b < ke) load(b, kb + 32 * b);
+                for (int k0 = kb; k0 < ke; k0 += 32 * C::kSteps) {
+#pragma unroll
+                    for (int b = 0; b < C::kSteps; ++b) {
+                        const int k = k0 + 32 * b, ahead = k + 32 * (C::kSteps - 1);
+                        if (ahead < ke) load((b + C::kSteps - 1) % C::kSteps, ahead);
+                        if (k < ke) multiply(b);
+                    }
                 }
             }
             __syncthreads();  // the last pass's sums have been read
@@ -323,10 +327,10 @@ size_t adapter_workspace(int T, int r) {
     return (size_t)T * r * 6 + (((size_t)T * 4 + 15) & ~size_t(15));
 }
 
-template <bool BF16, int WIN, int TERMS>
-static cudaError_t shrink(const AdapterArgs& p, cudaStream_t s) {
-    auto kern = shrink_kernel<BF16, WIN, TERMS>;
-    const int smem = ShrinkCfg<WIN>::kRed + WIN * p.r * 4;
+template <bool BF16, int WIN, int TERMS, int TILES>
+static cudaError_t shrink_tiles(const AdapterArgs& p, cudaStream_t s) {
+    auto kern = shrink_kernel<BF16, WIN, TERMS, TILES>;
+    const int smem = ShrinkCfg<WIN, TILES>::kRed + WIN * p.r * 4;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -344,6 +348,15 @@ static cudaError_t shrink(const AdapterArgs& p, cudaStream_t s) {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// as many rows of A a pass as the rank fills (32 tokens: two tiles leave room for the octets' accumulators)
+template <bool BF16, int WIN, int TERMS>
+static cudaError_t shrink(const AdapterArgs& p, cudaStream_t s) {
+    if (p.r <= 16) return shrink_tiles<BF16, WIN, TERMS, 1>(p, s);
+    if constexpr (WIN == 8)
+        if (p.r > 32) return shrink_tiles<BF16, WIN, TERMS, 4>(p, s);
+    return shrink_tiles<BF16, WIN, TERMS, 2>(p, s);
 }
 
 template <bool BF16, bool OUT32>

@@ -21,6 +21,7 @@ constexpr int32_t kMaxCols = 1 << 17;
 constexpr int32_t kMaxRank = moe::kMaxAdapterRank;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool good(const void* p) { return p && aligned16(p); }
 bool good_cols(int32_t n) { return n >= 8 && n % 8 == 0 && n <= kMaxCols; }
 // row pitch in values: whole 16-byte pieces, room for the row
@@ -48,7 +49,7 @@ moe_status moe_grouped_matmul(const void* x, int64_t ldx, int32_t rows, const vo
     const bool tr = (flags & MOE_OP_TRANSPOSE) != 0;
     if (!good_ld(ldx, tr ? n : k) || !good_ld(ldy, tr ? k : n)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!good(x) || !good(w) || !good(y) || !offsets || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+    if (!good(x) || !good(w) || !good(y) || !offsets || !aligned4(offsets))
         return MOE_ERR_INVALID_ARG;
     moe::GroupedArgs g{};
     g.offsets = offsets;
@@ -78,7 +79,7 @@ moe_status moe_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_
         if (acc) return MOE_OK;
         return cuda_status(cudaMemsetAsync(dw, 0, (size_t)n_groups * n * k * (f32 ? 4 : 2), s));
     }
-    if (!good(dy) || !good(x) || !offsets || (reinterpret_cast<uintptr_t>(offsets) & 3u)) return MOE_ERR_INVALID_ARG;
+    if (!good(dy) || !good(x) || !offsets || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
     moe::GroupedArgs g{};
     g.offsets = offsets;
     g.E = n_groups;
@@ -99,7 +100,7 @@ moe_status moe_swiglu(const void* gu, int64_t ldgu, int32_t rows, int32_t f, con
     if (rows < 0 || rows > kMaxRows || !good_cols(f) || !good_ld(ldgu, 2 * (int64_t)f) || !good_ld(ldh, f))
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!good(gu) || !good(h)) return MOE_ERR_INVALID_ARG;
+    if (!good(gu) || !good(h) || !aligned4(row_weights) || !aligned4(n_rows)) return MOE_ERR_INVALID_ARG;
     moe::SwigluArgs a{};
     a.gu = gu;
     a.ldgu = ldgu;
@@ -120,7 +121,9 @@ moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int
         !good_ld(lddgu, 2 * (int64_t)f) || (h && !good_ld(ldh, f)))
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!good(gu) || !good(dh) || !good(dgu) || (h && !aligned16(h))) return MOE_ERR_INVALID_ARG;
+    if (!good(gu) || !good(dh) || !good(dgu) || (h && !aligned16(h)) || !aligned4(row_weights) || !aligned4(n_rows) ||
+        !aligned4(d_row_weights))
+        return MOE_ERR_INVALID_ARG;
     moe::SwigluArgs a{};
     a.gu = gu;
     a.ldgu = ldgu;
@@ -151,7 +154,7 @@ moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, voi
         return MOE_ERR_INVALID_ARG;
     if (q.tokens == 0) return MOE_OK;
     if (!good(q.x) || !good(q.a) || !good(q.b) || !good(q.y) || !good(q.workspace) || (q.w && !aligned16(q.w)) ||
-        !q.ids || (reinterpret_cast<uintptr_t>(q.ids) & 3u) || (reinterpret_cast<uintptr_t>(q.scale) & 3u) ||
+        !q.ids || !aligned4(q.ids) || !aligned4(q.scale) ||
         q.workspace_bytes < moe_adapter_workspace(q.tokens, q.rank) || q.x == q.y)
         return MOE_ERR_INVALID_ARG;
     moe::AdapterArgs a{};

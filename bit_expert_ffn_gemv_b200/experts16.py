@@ -107,7 +107,8 @@ def grouped_matmul(x, w, offsets, out=None, transpose=False, out_dtype=None, str
     off = _vector(offsets, "offsets", dev, _INT32, E + 1)
     cols = k if transpose else n
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype or dt, device=x.device)
+        out = (x.new_empty((rows, cols)) if out_dtype is None
+               else torch.empty((rows, cols), dtype=out_dtype, device=x.device))
     odt = out.dtype
     if (odt is not dt and odt is not _FP32) or (out_dtype is not None and odt is not out_dtype):
         _fail(f"out: {odt}")
@@ -160,7 +161,7 @@ def swiglu(gu, row_weights=None, out=None, n_rows=None, stream=None):
     rw = _vector(row_weights, "row_weights", dev, _FP32, rows) if row_weights is not None else None
     nr = _vector(n_rows, "n_rows", dev, _INT32, 1) if n_rows is not None else None
     if out is None:
-        out = torch.empty((rows, f), dtype=dt, device=gu.device)
+        out = gu.new_empty((rows, f))
     ldh = _matrix(out, "out", dev, dt, rows, f)
     _enqueue(dev, stream, "moe_swiglu", lib().moe_swiglu, gu.data_ptr(), ld, rows, f, rw, nr, out.data_ptr(), ldh,
              MOE_OP_FP16 if dt is _FP16 else 0)
@@ -212,15 +213,14 @@ def adapter_project(x, a, b, ids, w=None, scale=None, out=None, flags=0, stream=
     if scale is not None:
         sp = _vector(scale, "scale", dev, _FP32, L)
     odt = _FP32 if flags & MOE_OUT_FP32 else dt
-    device = x.device
     if out is None:
         if flags & MOE_ACCUMULATE:
             _fail("MOE_ACCUMULATE adds to a given out")
-        out = torch.empty((T, n), dtype=odt, device=device)
+        out = x.new_empty((T, n)) if odt is dt else torch.empty((T, n), dtype=odt, device=x.device)
     ldy = _matrix(out, "out", dev, odt, T, n)
     L_ = lib()
     size = L_.moe_adapter_workspace(T, rank)
-    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    ws = x.new_empty(size // 2)  # (16-bit values)
     if stream is not None:
         ws.record_stream(stream)  # freed below, possibly before the call has run on its stream
     args = MoeAdapterArgs(x.data_ptr(), ldx, T, n, k, wp, a.data_ptr(), b.data_ptr(), sp, id_ptr, L, rank,

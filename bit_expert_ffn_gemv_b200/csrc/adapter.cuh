@@ -42,7 +42,7 @@ MOE_DEV uint16_t take_term(float& v) {
 // for its own tokens only (another adapter's infinities must not reach a token).
 // The next adapter's rows of B load behind the pass, and those of the tokens
 // after these (next .. next + n_next - 1) are fetched into L1.  Lane l / 4 reads
-// token l / 4 (+ 8) and feature rows l / 4 + 8 i; lane l % 4 takes four
+// token l / 4 (+ 8) and feature rows l / 4 + 8 i; lane l % 4 takes eight
 // consecutive rank values of each, the same for both operands.
 template <bool BF16, int TERMS>
 MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next, int f0, uint32_t* lo, uint32_t* hi) {
@@ -69,27 +69,22 @@ MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next
     }
     int64_t at[4];  // offset of feature rows f0 + gq + 8 i in one adapter's B (past N: any row, not stored)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = (int64_t)min(f0 + gq + 8 * i, p.N - 1) * p.r + 4 * c;
+    for (int i = 0; i < 4; ++i) at[i] = (int64_t)min(f0 + gq + 8 * i, p.N - 1) * p.r + 8 * c;
     for (int j0 = 0; j0 < p.r; j0 += 32) {
-        uint2 v[2][2][TERMS], w[2][4], w_next[2][4];
+        const bool in = j0 + 8 * c < p.r;
+        uint4 v[2][TERMS], w[4], w_next[4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int k = 0; k < TERMS; ++k) {
-                    v[s][q][k] = make_uint2(0, 0);
-                    if (j0 + 16 * s + 4 * c < p.r && use[q])
-                        v[s][q][k] = *reinterpret_cast<const uint2*>(adapter_term(p, k) + (int64_t)(t0 + gq + 8 * q) * p.r + j0 +
-                                                                     16 * s + 4 * c);
-                }
-        auto load = [&](int a, uint2 (&to)[2][4]) {
+            for (int k = 0; k < TERMS; ++k) {
+                v[q][k] = make_uint4(0, 0, 0, 0);
+                if (in && use[q])
+                    v[q][k] = *reinterpret_cast<const uint4*>(adapter_term(p, k) + (int64_t)(t0 + gq + 8 * q) * p.r + j0 + 8 * c);
+            }
+        auto load = [&](int a, uint4 (&to)[4]) {
             const uint16_t* rows = B + (int64_t)a * p.N * p.r + j0;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    to[s][i] = j0 + 16 * s + 4 * c < p.r ? __ldg(reinterpret_cast<const uint2*>(rows + at[i] + 16 * s)) : make_uint2(0, 0);
+            for (int i = 0; i < 4; ++i) to[i] = load_or_zero(rows + at[i], in);
         };
         uint32_t todo = all;
         int leader = __ffs(todo) - 1;
@@ -105,15 +100,14 @@ MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next
             for (int q = 0; q < 2; ++q) {
                 if (!((used >> (8 * q)) & 0xffu)) continue;
                 float d[2][4] = {};
+                const uint32_t lo0[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, lo1[4] = {w[0].z, w[1].z, w[0].w, w[1].w};
+                const uint32_t hi0[4] = {w[2].x, w[3].x, w[2].y, w[3].y}, hi1[4] = {w[2].z, w[3].z, w[2].w, w[3].w};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t fa[4] = {w[s][0].x, w[s][1].x, w[s][0].y, w[s][1].y};
-                    const uint32_t fb[4] = {w[s][2].x, w[s][3].x, w[s][2].y, w[s][3].y};
-#pragma unroll
-                    for (int k = 0; k < TERMS; ++k) {
-                        mma16<BF16>(d[0], fa, v[s][q][k].x, v[s][q][k].y);
-                        mma16<BF16>(d[1], fb, v[s][q][k].x, v[s][q][k].y);
-                    }
+                for (int k = 0; k < TERMS; ++k) {
+                    mma16<BF16>(d[0], lo0, v[q][k].x, v[q][k].y);
+                    mma16<BF16>(d[1], hi0, v[q][k].x, v[q][k].y);
+                    mma16<BF16>(d[0], lo1, v[q][k].z, v[q][k].w);
+                    mma16<BF16>(d[1], hi1, v[q][k].z, v[q][k].w);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -124,9 +118,7 @@ MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next
                 }
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[s][i] = w_next[s][i];
+            for (int i = 0; i < 4; ++i) w[i] = w_next[i];
         }
     }
 }

@@ -35,11 +35,11 @@ namespace moe {
 constexpr int kShrinkThreads = 256;
 
 // Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K
-// whose operands are in registers at once: as many as 64 to 72 registers hold.
+// whose operands are in registers at once: as many as about 50 registers hold.
 template <int WIN, int TILES>
 struct ShrinkCfg {
     static constexpr int kOctets = WIN / 8, kTiles = TILES, kRows = 16 * TILES, kPitch = kRows + 4;
-    static constexpr int kVecs = kOctets + 2 * TILES, kSteps = 4 * kVecs <= 18 ? 4 : 3 * kVecs <= 18 ? 3 : 2;
+    static constexpr int kVecs = kOctets + 2 * TILES, kSteps = 4 * kVecs <= 12 ? 4 : 2;
     static constexpr int kRed = 8 * WIN * kPitch * 4;  // bytes: [warp][token of its item][row]
 };
 
@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
     float* red = reinterpret_cast<float*>(shrink_smem);                 // [8][WIN][kPitch]
     float* sums = reinterpret_cast<float*>(shrink_smem + C::kRed);      // [WIN][r]
     __shared__ int item_adapter[WIN], item_count[WIN];
-    __shared__ int8_t item_tok[WIN][WIN];
+    __shared__ int8_t item_tok[WIN][WIN];          // tokens of an item, in order
+    __shared__ int8_t tok_item[WIN], tok_place[WIN];  // a token's item (-1: none) and place in it
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, c = lane & 3;
     const int t0 = blockIdx.x * WIN, slice = blockIdx.y;
@@ -64,12 +65,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
     const uint32_t starts = __ballot_sync(0xffffffffu, begins);
     const int items = __popc(starts);
     if (items == 0) return;  // (the whole cluster)
-    if (warp == 0 && begins) {
-        const int it = __popc(starts & ((1u << lane) - 1));
-        item_adapter[it] = id;
-        int n = 0;
-        for (uint32_t rest = mine; rest; rest &= rest - 1) item_tok[it][n++] = (int8_t)(__ffs(rest) - 1);
-        item_count[it] = n;
+    if (warp == 0 && lane < WIN) {
+        const uint32_t below = (1u << lane) - 1;
+        const int it = __popc(starts & ((1u << (__ffs(mine) - 1)) - 1)), place = __popc(mine & below);
+        tok_item[lane] = (int8_t)(id >= 0 ? it : -1);
+        tok_place[lane] = (int8_t)place;
+        if (id >= 0) item_tok[it][place] = (int8_t)lane;
+        if (begins) {
+            item_adapter[it] = id;
+            item_count[it] = __popc(mine);
+        }
     }
     __syncthreads();
     const int share = items == 1 ? 8 : items == 2 ? 4 : items <= 4 ? 2 : 1;  // warps per item
@@ -151,17 +156,17 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                     m[C::kPitch + 8] = acc[q][o][3];
                 }
             __syncthreads();
-            // the shares of each item, added in order
-            for (int i = warp; i < at_once * WIN; i += 8) {
-                const int slot = i / WIN, m = i % WIN, ii = base + slot;
-                if (ii >= items || m >= item_count[ii]) continue;
-                const float* src = red + (slot * share * WIN + m) * C::kPitch;
-                float* dst = sums + item_tok[ii][m] * p.r + j0;
-                for (int j = lane; j < rows; j += 32) {
-                    float s = src[j];
-                    for (int q = 1; q < share; ++q) s += src[q * WIN * C::kPitch + j];
-                    dst[j] = s;
-                }
+            // each token's sums, the shares added in order
+#pragma unroll
+            for (int i = tid; i < WIN * C::kRows; i += kShrinkThreads) {
+                const int m = i / C::kRows, j = i % C::kRows, slot = tok_item[m] - base;
+                if (j >= rows || tok_item[m] < 0 || slot < 0 || slot >= at_once) continue;
+                const float* src = red + (slot * share * WIN + tok_place[m]) * C::kPitch + j;
+                float s = src[0];
+#pragma unroll
+                for (int q = 1; q < 8; ++q)
+                    if (q < share) s += src[q * WIN * C::kPitch];
+                sums[m * p.r + j0 + j] = s;
             }
         }
     }
@@ -222,66 +227,76 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
 
 // ---------------------------------------------------------------- the delta alone
 // CTA: 16 tokens by 256 features, a warp 64 of them.  Tokens are the MMA's M, so
-// that a lane holds pairs of adjacent features: y moves in 8-byte (fp32) or
-// 4-byte pieces that fill 32-byte sectors, and v's fragments serve all 64
-// features.  Everything independent of v is loaded before the wait for it.
+// that v's fragments serve all 64 features; the features' order over the MMA's
+// columns gives a lane four adjacent ones of a pair of column tiles, so y moves
+// 16 (fp32) or 8 bytes a lane, and both operands load 16 bytes a lane (32 rank
+// values a row) in the same permuted order.  y and the ids are read before the
+// wait for v.
 template <bool BF16, bool OUT32>
 __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
-    constexpr int TERMS = BF16 && OUT32 ? 3 : 2, NT = 8;
+    constexpr int TERMS = BF16 && OUT32 ? 3 : 2, PAIRS = 4;  // pairs of column tiles: 16 features each
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
-    const int f0 = (blockIdx.y * 4 + warp) * 64, t0 = blockIdx.x * 16, n = min(16, p.T - t0);
+    const int f0 = (blockIdx.y * 4 + warp) * 16 * PAIRS, t0 = blockIdx.x * 16, n = min(16, p.T - t0);
     if (f0 >= p.N) return;
     int id = lane < n ? __ldg(&p.ids[t0 + lane]) : -1;
     if (id < 0 || id >= p.L) id = -1;
     const uint32_t mine = __match_any_sync(0xffffffffu, id);
     uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
-    float y[NT][4];  // [8 features][token gq: features 2c, 2c + 1; token gq + 8: the same]
+    // y[pair][h][i]: token gq + 8 h, feature f0 + 16 pair + 4 c + i
+    float y[PAIRS][2][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < PAIRS; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int f = f0 + 8 * t + 2 * c;
-            float2 v = make_float2(0.f, 0.f);
+            const int f = f0 + 16 * t + 4 * c;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (p.accumulate && gq + 8 * h < n && f < p.N) {
                 const int64_t o = (int64_t)(t0 + gq + 8 * h) * p.ldy + f;
-                if (OUT32) v = *reinterpret_cast<const float2*>(static_cast<const float*>(p.y) + o);
-                else v = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.y) + o));
+                if (OUT32) {
+                    v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.y) + o);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.y) + o);
+                    const float2 a = unpack2<BF16>(u.x), b = unpack2<BF16>(u.y);
+                    v = make_float4(a.x, a.y, b.x, b.y);
+                }
             }
-            y[t][2 * h] = v.x;
-            y[t][2 * h + 1] = v.y;
+            y[t][h][0] = v.x, y[t][h][1] = v.y, y[t][h][2] = v.z, y[t][h][3] = v.w;
         }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int quads = p.r >> 2;
+    const int fl = 4 * (gq >> 1) + (gq & 1);  // column gq of a pair's first tile is this feature, of the second 2 more
     while (todo) {  // one pass per distinct adapter of the 16 tokens
         const int leader = __ffs(todo) - 1;
         const int a = __shfl_sync(0xffffffffu, id, leader);
         const uint32_t used = __shfl_sync(0xffffffffu, mine, leader);
         todo &= ~used;
         const bool use[2] = {((used >> gq) & 1) != 0, ((used >> (8 + gq)) & 1) != 0};
-        const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)a * p.N + f0 + gq) * p.r;
-        const int64_t vrow = (int64_t)(t0 + gq) * p.r;
-        float d[NT][4] = {};
-#pragma unroll 2
-        for (int q0 = 0; q0 < quads; q0 += 4) {
-            const int q = q0 + c;
-            uint2 v[2][TERMS], w[NT];
+        const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)a * p.N + f0 + fl) * p.r + 8 * c;
+        const int64_t vrow = (int64_t)(t0 + gq) * p.r + 8 * c;
+        float d[2 * PAIRS][4] = {};
+        for (int j0 = 0; j0 < p.r; j0 += 32) {
+            const bool in = j0 + 8 * c < p.r;
+            uint4 v[2][TERMS], w[2 * PAIRS];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                w[t] = q < quads && f0 + 8 * t + gq < p.N ? __ldg(reinterpret_cast<const uint2*>(B + (int64_t)8 * t * p.r + 4 * q))
-                                                          : make_uint2(0, 0);
+            for (int t = 0; t < 2 * PAIRS; ++t) {
+                const int f = 16 * (t >> 1) + 2 * (t & 1);
+                w[t] = load_or_zero(B + (int64_t)f * p.r + j0, in && f0 + fl + f < p.N);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int k = 0; k < TERMS; ++k) {
-                    v[h][k] = make_uint2(0, 0);
-                    if (q < quads && use[h])
-                        v[h][k] = *reinterpret_cast<const uint2*>(adapter_term(p, k) + vrow + (int64_t)h * 8 * p.r + 4 * q);
+                    v[h][k] = make_uint4(0, 0, 0, 0);
+                    if (in && use[h]) v[h][k] = *reinterpret_cast<const uint4*>(adapter_term(p, k) + vrow + (int64_t)h * 8 * p.r + j0);
                 }
 #pragma unroll
             for (int k = 0; k < TERMS; ++k) {
-                const uint32_t av[4] = {v[0][k].x, v[1][k].x, v[0][k].y, v[1][k].y};
+                const uint32_t a0[4] = {v[0][k].x, v[1][k].x, v[0][k].y, v[1][k].y};
+                const uint32_t a1[4] = {v[0][k].z, v[1][k].z, v[0][k].w, v[1][k].w};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma16<BF16>(d[t], av, w[t].x, w[t].y);
+                for (int t = 0; t < 2 * PAIRS; ++t) {
+                    mma16<BF16>(d[t], a0, w[t].x, w[t].y);
+                    mma16<BF16>(d[t], a1, w[t].z, w[t].w);
+                }
             }
         }
 #pragma unroll
@@ -289,29 +304,34 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
             if (!use[h]) continue;  // (another adapter's infinities must not reach this token)
             const float back = BF16 ? 1.f : adapter_back(p, TERMS)[t0 + gq + 8 * h];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                y[t][2 * h] += BF16 ? d[t][2 * h] : d[t][2 * h] * back;
-                y[t][2 * h + 1] += BF16 ? d[t][2 * h + 1] : d[t][2 * h + 1] * back;
-            }
+            for (int t = 0; t < PAIRS; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = d[2 * t + (i >> 1)][2 * h + (i & 1)];
+                    y[t][h][i] = BF16 ? y[t][h][i] + v : fmaf(v, back, y[t][h][i]);
+                }
         }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < PAIRS; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int f = f0 + 8 * t + 2 * c;
+            const int f = f0 + 16 * t + 4 * c;
             if (gq + 8 * h < n && f < p.N) {
                 const int64_t o = (int64_t)(t0 + gq + 8 * h) * p.ldy + f;
-                if (OUT32) *reinterpret_cast<float2*>(static_cast<float*>(p.y) + o) = make_float2(y[t][2 * h], y[t][2 * h + 1]);
-                else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + o) = pack2<BF16>(y[t][2 * h], y[t][2 * h + 1]);
+                const float* v = y[t][h];
+                if (OUT32) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + o) = make_float4(v[0], v[1], v[2], v[3]);
+                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + o) = make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
             }
         }
 }
 
 // ---------------------------------------------------------------- launcher
-// Up to this many tokens a window is 8 tokens: a decode batch is mostly
-// tokens of different adapters, and more windows share its A rows out.
-constexpr int kSmallWindowTokens = 256;
+// A window is 8 tokens while such windows fit the 148 SMs once, else 32.  Small
+// windows share a mixed batch's A rows out over more CTAs (512 tokens of 30
+// adapters, rank 16: 22 us against 29), large ones read the A rows of a long
+// run less often (8192 tokens of one adapter, rank 64: 25 us against 39).
+constexpr int kSmallWindowTokens = 148 * 8;
 
 // CTAs that split a window's K: a power of two up to 8, so that the windows'
 // CTAs fill the GPU once while each keeps at least 256 of K.

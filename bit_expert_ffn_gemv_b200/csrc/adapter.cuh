@@ -52,7 +52,6 @@ MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next
     if (id < 0 || id >= p.L) id = -1;
     if (id_next < 0 || id_next >= p.L) id_next = -1;
     const uint16_t* B = static_cast<const uint16_t*>(p.b);
-    const int quads = p.r >> 2;
     const uint32_t mine = __match_any_sync(0xffffffffu, id), mine_next = __match_any_sync(0xffffffffu, id_next);
     if (id_next >= 0 && (mine_next & ((1u << lane) - 1)) == 0) {  // an adapter's first token: its 32 rows are contiguous
         const char* rows = reinterpret_cast<const char*>(B + ((int64_t)id_next * p.N + f0) * p.r);

@@ -49,8 +49,7 @@ moe_status moe_grouped_matmul(const void* x, int64_t ldx, int32_t rows, const vo
     const bool tr = (flags & MOE_OP_TRANSPOSE) != 0;
     if (!good_ld(ldx, tr ? n : k) || !good_ld(ldy, tr ? k : n)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!good(x) || !good(w) || !good(y) || !offsets || !aligned4(offsets))
-        return MOE_ERR_INVALID_ARG;
+    if (!good(x) || !good(w) || !good(y) || x == y || w == y || !offsets || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
     moe::GroupedArgs g{};
     g.offsets = offsets;
     g.E = n_groups;

@@ -8,9 +8,9 @@
 // computed.  The warps' sums meet in shared memory in warp order
 // (deterministic).  Bound by HBM: 2 N K bytes per matrix.
 //
-// Grouped form: a row's CTA looks its group up in the offsets (one round of
-// loads) and works only if it is the group's first row, so no list of groups
-// is built beforehand.  Adapter form: one matrix, then the tokens' deltas.
+// Grouped form: a CTA finds the group it works for in the offsets (one round of
+// loads and a prefix count of those that hold rows), so no list of groups is
+// built beforehand.  Adapter form: one matrix, then the tokens' deltas.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -99,20 +99,45 @@ template <bool BF16, bool OUT32, bool ADAPT, int MAXNB>
 __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyArgs p) {
     constexpr int kPitch = 8 * MAXNB + 1;
     __shared__ __align__(16) float red[8][16 * kPitch];
-    __shared__ int found[3];
+    __shared__ int found[3], counts[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
     int e = 0, row0 = 0, n = ADAPT ? p.ad.T : 0;
     if (!ADAPT) {
-        const int r = blockIdx.y;
+        // this CTA's group: the blockIdx.y-th that holds rows (a thread looks at up to four)
+        constexpr int kMost = 4;
+        const int each = (p.E + kSkinnyThreads - 1) / kSkinnyThreads, first = tid * each;
+        int lo[kMost], hi[kMost], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            lo[i] = hi[i] = 0;
+            if (i < each && first + i < p.E) {
+                lo[i] = min(max(__ldg(&p.offsets[first + i]), 0), p.M);
+                hi[i] = min(max(__ldg(&p.offsets[first + i + 1]), 0), p.M);
+            }
+            mine += hi[i] > lo[i];
+        }
+        int before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += u;
+        }
+        if (lane == 31) counts[warp] = before;
         if (tid == 0) found[1] = -1;
         __syncthreads();
-        for (int i = tid; i < p.E; i += kSkinnyThreads) {
-            const int a = min(max(__ldg(&p.offsets[i]), 0), p.M), b = min(max(__ldg(&p.offsets[i + 1]), 0), p.M);
-            if (a == r && b > r) {  // (a table that is not ascending may name a row twice: one group wins)
-                found[0] = i;
-                found[1] = a;
-                found[2] = b - a;
+        before -= mine;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < warp) before += counts[q];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            if (hi[i] <= lo[i]) continue;
+            if (before == (int)blockIdx.y) {
+                found[0] = first + i;
+                found[1] = lo[i];
+                found[2] = hi[i] - lo[i];
             }
+            ++before;
         }
         __syncthreads();
         if (found[1] < 0) return;
@@ -230,7 +255,7 @@ cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const voi
     p.M = g.M;
     p.y = g.out;
     p.ldy = g.ldo;
-    const dim3 grid((g.F + 15) / 16, g.M);
+    const dim3 grid((g.F + 15) / 16, g.E < g.M ? g.E : g.M);  // (groups that hold rows, at most)
     if (g.bf16) return out32 ? skinny<true, true, false>(p, g.M, grid, s) : skinny<true, false, false>(p, g.M, grid, s);
     return out32 ? skinny<false, true, false>(p, g.M, grid, s) : skinny<false, false, false>(p, g.M, grid, s);
 }

@@ -16,13 +16,13 @@ def L():
     return moe.lib()
 
 
-GOOD_MATMUL = dict(x=P, ldx=64, rows=10, w=P, offsets=P, groups=4, n=32, k=64, y=P, ldy=32, flags=0)
+GOOD_MATMUL = dict(x=P, ldx=64, rows=10, w=3 * P, offsets=P, groups=4, n=32, k=64, y=2 * P, ldy=32, flags=0)
 
 
 @pytest.mark.parametrize("bad", [
     dict(rows=-1), dict(rows=(1 << 27) + 1), dict(groups=0), dict(groups=1025), dict(n=0), dict(n=12), dict(k=4), dict(k=-8),
     dict(n=1 << 18), dict(ldx=56), dict(ldx=68), dict(ldy=24), dict(ldy=36), dict(x=0), dict(x=P + 8), dict(w=0), dict(w=P + 2),
-    dict(y=0), dict(y=P + 4), dict(offsets=0), dict(offsets=P + 2), dict(flags=0x2), dict(flags=0x4), dict(flags=1 << 31),
+    dict(y=0), dict(y=P + 4), dict(y=P), dict(y=3 * P), dict(offsets=0), dict(offsets=P + 2), dict(flags=0x2), dict(flags=0x4), dict(flags=1 << 31),
     dict(flags=0x200),  # transposed: x needs n columns a row, y needs k
 ], ids=str)
 def test_grouped_matmul(L, bad):

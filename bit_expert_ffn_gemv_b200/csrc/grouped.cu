@@ -820,7 +820,11 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& args, const void* w, con
                         : grouped_launch<kGroupedWeights, false, false>(g, m, tiles, s);
     }
     const bool forward = mode == kGroupedForward;
-    if (forward && g.M <= kSkinnyMaxRows) return launch_skinny_grouped(g, w, x, ldx, out_fp32, s);
+    // Few rows: the warp-MMA kernel while the tiles would not give every pair of SMs one, which costs the
+    // tensor-core kernel its start-up and leaves SMs idle (64 rows of one 2048 x 2048 matrix: 8.2 us against
+    // 12.5; of 64 such matrices: 78 us against 58, its CTAs living too short for HBM).
+    if (forward && g.M <= kSkinnyMaxRows && (g.E < g.M ? g.E : g.M) * JT < sm_count() / 2)
+        return launch_skinny_grouped(g, w, x, ldx, out_fp32, s);
     e = product_maps(&m, forward, bf, g.E, forward ? g.F : g.C, forward ? g.C : g.F, w, forward ? x : dy, g.M,
                      forward ? ldx : lddy);
     if (e != cudaSuccess) return e;

@@ -201,7 +201,7 @@ struct SwigluArgs {
 };
 cudaError_t launch_swiglu(const SwigluArgs& a, bool bf16, bool grad, cudaStream_t s);
 
-// Products of at most this many rows take the warp-MMA kernel (skinny.cu).
+// Products of at most this many rows can take the warp-MMA kernel (skinny.cu).
 constexpr int kSkinnyMaxRows = 64;
 cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const void* x, int64_t ldx, bool out32,
                                   cudaStream_t s);

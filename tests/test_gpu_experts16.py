@@ -37,7 +37,8 @@ def _groups(h, x):
 
 
 def _rel(a, b):
-    return float((a.double() - b.double()).norm() / b.double().norm())
+    a, b = a.detach().double(), b.detach().double()
+    return float((a - b).norm() / b.norm())
 
 
 def test_dequantised_experts_give_the_quantised_layer():

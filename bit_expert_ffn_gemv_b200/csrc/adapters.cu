@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
     __shared__ int item_adapter[WIN], item_count[WIN];
     __shared__ int8_t item_tok[WIN][WIN];          // tokens of an item, in order
     __shared__ int8_t tok_item[WIN], tok_place[WIN];  // a token's item (-1: none) and place in it
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();     // the kernel before may still write x and ids, or read v
+    grid_release();  // (after the wait: the next kernel reads W, x and ids at once)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, c = lane & 3;
     const int t0 = blockIdx.x * WIN, slice = blockIdx.y;
     const int per = ((p.K + p.slices - 1) / p.slices + 31) & ~31;  // K of a CTA
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
             }
             y[t][h][0] = v.x, y[t][h][1] = v.y, y[t][h][2] = v.z, y[t][h][3] = v.w;
         }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     const int fl = 4 * (gq >> 1) + (gq & 1);  // column gq of a pair's first tile is this feature, of the second 2 more
     while (todo) {  // one pass per distinct adapter of the 16 tokens
         const int leader = __ffs(todo) - 1;
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
                 }
         }
     }
+    grid_release();
 #pragma unroll
     for (int t = 0; t < PAIRS; ++t)
 #pragma unroll
@@ -355,18 +357,20 @@ static cudaError_t shrink_tiles(const AdapterArgs& p, cudaStream_t s) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 1;
-    at.val.clusterDim.y = (unsigned)p.slices;
-    at.val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = (unsigned)p.slices;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((p.T + WIN - 1) / WIN, p.slices);
     cfg.blockDim = kShrinkThreads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -390,16 +394,7 @@ static cudaError_t adapters(AdapterArgs p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (skinny) return launch_skinny_adapter(p, BF16, OUT32, s);
     if (p.w) return launch_grouped_adapter(p, BF16, OUT32, s);
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((p.T + 15) / 16, (p.N + 255) / 256);
-    cfg.blockDim = 128;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expand_kernel<BF16, OUT32>, p);
+    return launch_behind(expand_kernel<BF16, OUT32>, dim3((p.T + 15) / 16, (p.N + 255) / 256), 128, 0, s, p);
 }
 
 cudaError_t launch_adapters(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {

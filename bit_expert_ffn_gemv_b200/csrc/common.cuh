@@ -208,8 +208,34 @@ MOE_DEV void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 MOE_DEV void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 MOE_DEV void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
+// ---------------------------------------------------------------- programmatic dependent launch
+// A kernel launched with launch_behind() may start while the kernel before it on
+// the stream still runs; nothing that kernel writes or reads may be touched
+// before grid_wait(), which returns once it has completed.  grid_release() lets
+// the next such kernel start as soon as every CTA of this one has called it.
+MOE_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MOE_DEV void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 MOE_DEV float silu(float g) { return g / (1.0f + __expf(-g)); }
 
 MOE_DEV float bf16_bits_to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+#ifdef __CUDACC__
+template <class... Params, class... Args>
+inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                 Args&&... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+#endif
 
 }  // namespace moe

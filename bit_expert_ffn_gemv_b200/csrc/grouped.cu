@@ -224,6 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     if (warp == 2) tc::tmem_alloc_pair(&tmem_slot, 512);
     if (warp == 3 && lane < 3) tc::prefetch_map(lane == 0 ? &amap : lane == 1 ? &bmap : &cmap);
 
+    if (!ADAPT) grid_wait();  // (adapters: W, x and ids are older than the kernel before, which only makes v)
     // (the loops below stay rolled: this part runs once, and its instructions come from memory)
     int E = g.E;
     bool runs = false;  // adapters: every tile has one adapter
@@ -338,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             one_adapter = runs ? adapter_of(ex.args, tl.row0) : -1;
             if (one_adapter < 0) return 0;
             if (!g.bf16) {
-                asm volatile("griddepcontrol.wait;" ::: "memory");
+                grid_wait();
                 if (!unscaled(ex.args, terms, tl.row0, tl.n)) return 0;
             }
             return terms * rank_blocks;
@@ -370,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 const bool tail = WG && s == KS - 1 && (tl.n & 15);
                 const uint32_t bar = (tail ? tail_own : full_leader) + (uint32_t)st * 8u;
                 if (ADAPT && s == KC) {
-                    asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
+                    grid_wait();  // v, from the kernel before
                     fence_proxy_async_global();
                 }
                 if (one) {
@@ -416,6 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                 }
             }
         }
+        grid_release();  // (late: the next kernel's CTAs then find most SMs free, not the first few)
         if (!ok) tc::settle();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -500,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         bool ok = true;
         int it = 0;
         const bool bf16 = g.bf16 != 0;
-        if (ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");  // v, from the kernel before
+        if (ADAPT) grid_wait();  // v, from the kernel before
         for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
             const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
             const bool empty = WG && tl.n == 0;
@@ -728,8 +730,7 @@ static cudaError_t grouped_launch(const GroupedArgs& g, const GroupedMaps& m, in
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(most_tiles < sm_count() / 2 ? most_tiles : sm_count() / 2);
-    kern<<<2 * pairs, kGroupedThreads, smem, s>>>(g, GroupedExtra<false>{}, m.a, m.b, m.c);
-    return cudaGetLastError();
+    return launch_behind(kern, 2 * pairs, kGroupedThreads, smem, s, g, GroupedExtra<false>{}, m.a, m.b, m.c);
 }
 
 // maps of the forward and rows products: W as [E][N][K], whose rows (forward) or columns are the features
@@ -779,17 +780,8 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     if (e != cudaSuccess) return e;
     // (runs cut blocks off: at most one block more per run of 32 tokens)
     const int64_t tiles = (int64_t)((p.T + g.block - 1) / g.block + p.T / 32) * ((p.N + 255) / 256);
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * (unsigned)(tiles < sm_count() / 2 ? tiles : sm_count() / 2));
-    cfg.blockDim = kGroupedThreads;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, g, ex, m.a, m.b, m.c);
+    const int pairs = (int)(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
+    return launch_behind(kern, 2 * pairs, kGroupedThreads, smem, s, g, ex, m.a, m.b, m.c);
 }
 
 cudaError_t launch_grouped_adapter(const AdapterArgs& p, bool bf16, bool out32, cudaStream_t s) {

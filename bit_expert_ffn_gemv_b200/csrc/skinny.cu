@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
     constexpr int kPitch = 8 * MAXNB + 1;
     __shared__ __align__(16) float red[8][16 * kPitch];
     __shared__ int found[3], counts[8];
+    if (!ADAPT) grid_wait();  // (adapters: W, x and ids are older than the kernel before, which only makes v)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2;
     int e = 0, row0 = 0, n = ADAPT ? p.ad.T : 0;
     if (!ADAPT) {
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
     else if (MAXNB == 8 && n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     else if (MAXNB == 8) skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     __syncthreads();
+    grid_release();  // (late: the next kernel's CTAs then spread over the SMs as evenly as this one's)
     // thread: feature tid % 16, rows tid / 16 + 16 i
     constexpr int kOut = (16 * 8 * MAXNB + kSkinnyThreads - 1) / kSkinnyThreads;
     const int j = tid & 15, f = f0 + j, m0 = tid >> 4;
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
                 if (ad.r > 8) ahead[i][1] = __ldg(reinterpret_cast<const uint4*>(br[i] + 8));
             }
         }
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        grid_wait();
         constexpr int kBlock = 64;  // rank values per pass
         float* v = &red[0][0];      // [row][kBlock]: the sums above are in registers
         static_assert(8 * MAXNB * kBlock <= 8 * 16 * kPitch, "v fits over the sums");
@@ -230,16 +232,7 @@ static cudaError_t skinny(const SkinnyArgs& p, int rows, dim3 grid, cudaStream_t
     auto kern = rows <= 8    ? skinny_kernel<BF16, OUT32, ADAPT, 1>
                 : rows <= 16 ? skinny_kernel<BF16, OUT32, ADAPT, 2>
                              : skinny_kernel<BF16, OUT32, ADAPT, 8>;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = kSkinnyThreads;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = ADAPT ? 1 : 0;  // behind the inner values' kernel
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return launch_behind(kern, grid, kSkinnyThreads, 0, s, p);
 }
 
 cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const void* x, int64_t ldx, bool out32,

@@ -25,6 +25,8 @@ constexpr int kSwigluFewRows = 148 * 8 * 4;  // below this many rows a whole blo
 
 template <bool BF16, int WARPS>
 __global__ void __launch_bounds__(kSwigluThreads) swiglu_kernel(const SwigluArgs a) {
+    grid_release();
+    grid_wait();
     const int per = 8 / WARPS, lanes = WARPS * 32;
     const int r = blockIdx.x * per + (WARPS == 1 ? threadIdx.x >> 5 : 0);
     const int lane = threadIdx.x & (lanes - 1);
@@ -49,6 +51,8 @@ __global__ void __launch_bounds__(kSwigluThreads) swiglu_kernel(const SwigluArgs
 template <bool BF16, int WARPS>
 __global__ void __launch_bounds__(kSwigluThreads) swiglu_grad_kernel(const SwigluArgs a) {
     __shared__ float part[8];
+    grid_release();
+    grid_wait();
     const int per = 8 / WARPS, lanes = WARPS * 32;
     const int r = blockIdx.x * per + (WARPS == 1 ? threadIdx.x >> 5 : 0);
     const int lane = threadIdx.x & (lanes - 1);
@@ -95,22 +99,16 @@ __global__ void __launch_bounds__(kSwigluThreads) swiglu_grad_kernel(const Swigl
 }
 
 template <bool BF16>
-static void launch(const SwigluArgs& a, bool grad, cudaStream_t s) {
+static cudaError_t launch(const SwigluArgs& a, bool grad, cudaStream_t s) {
     const bool few = a.M < kSwigluFewRows;
     const int blocks = few ? a.M : (a.M + 7) / 8;
-    if (grad) {
-        if (few) swiglu_grad_kernel<BF16, 8><<<blocks, kSwigluThreads, 0, s>>>(a);
-        else swiglu_grad_kernel<BF16, 1><<<blocks, kSwigluThreads, 0, s>>>(a);
-    } else {
-        if (few) swiglu_kernel<BF16, 8><<<blocks, kSwigluThreads, 0, s>>>(a);
-        else swiglu_kernel<BF16, 1><<<blocks, kSwigluThreads, 0, s>>>(a);
-    }
+    auto kern = grad ? (few ? swiglu_grad_kernel<BF16, 8> : swiglu_grad_kernel<BF16, 1>)
+                     : (few ? swiglu_kernel<BF16, 8> : swiglu_kernel<BF16, 1>);
+    return launch_behind(kern, blocks, kSwigluThreads, 0, s, a);
 }
 
 cudaError_t launch_swiglu(const SwigluArgs& a, bool bf16, bool grad, cudaStream_t s) {
-    if (bf16) launch<true>(a, grad, s);
-    else launch<false>(a, grad, s);
-    return cudaGetLastError();
+    return bf16 ? launch<true>(a, grad, s) : launch<false>(a, grad, s);
 }
 
 }  // namespace moe

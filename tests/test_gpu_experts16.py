@@ -260,3 +260,46 @@ def test_wrappers_refuse():
         moe.grouped_matmul(torch.zeros(6, 80, dtype=bf, device=dev)[:, 4:68], w, off)
     with pytest.raises(moe.MoeError):  # a result that is also the input
         moe.adapter_project(dh, torch.zeros(2, 8, 32, dtype=bf, device=dev), b, ids, out=dh)
+
+
+@pytest.mark.parametrize("rows", [40, 300, 3000])
+def test_back_to_back_calls_are_ordered(rows):
+    """Kernels of these calls may start before the one before them has finished: a chain in which every call reads what
+    the one before wrote, and overwrites what it read, gives the same bits as with a synchronisation after each call."""
+    E, d, f, L, r = 6, 256, 128, 4, 16
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def normal(*shape, s=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * s).bfloat16()
+
+    w1, w2, w = normal(E, 2 * f, d, s=d ** -0.5), normal(E, d, f, s=f ** -0.5), normal(d, d, s=d ** -0.5)
+    a, b, rw = normal(L, r, d, s=d ** -0.5), normal(L, d, r, s=0.2), torch.rand(rows, generator=g, device="cuda")
+    cuts = torch.randint(0, rows + 1, (E - 1,), generator=g, device="cuda").sort().values
+    off = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), rows)]).int()
+    ids = torch.randint(-1, L, (rows,), generator=g, device="cuda").sort().values.int()
+    x0 = normal(rows, d)
+
+    def chain(wait):
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+        x, gu, h = x0.clone(), torch.empty(rows, 2 * f, dtype=x0.dtype, device="cuda"), torch.empty(rows, f, dtype=x0.dtype, device="cuda")
+        y, dw = torch.empty_like(x), torch.zeros(E, 2 * f, d, device="cuda")
+        done()
+        for k in range(12):
+            moe.grouped_matmul(x, w1, off, out=gu), done()
+            moe.swiglu(gu, rw, out=h), done()
+            moe.grouped_matmul(h, w2, off, out=y), done()
+            moe.adapter_project(y, a, b, ids, w=w, out=x), done()
+            moe.adapter_project(y, a, b, ids, out=x, flags=moe.MOE_ACCUMULATE), done()
+            moe.swiglu_backward(gu, h, rw, dgu=gu.clone() if k % 2 else gu), done()
+            moe.grouped_matmul_wgrad(gu, x, off, out=dw, accumulate=True), done()
+            moe.grouped_matmul(y, w2, off, out=h, transpose=True), done()
+            x.add_(moe.rms_normalize(y)), done()
+            x.copy_(moe.rms_normalize(x)), done()
+        return x, y, h, gu, dw
+
+    plain = chain(True)
+    for _ in range(4):
+        for p, q in zip(plain, chain(False)):
+            assert torch.equal(p, q)

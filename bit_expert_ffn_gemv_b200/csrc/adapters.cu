@@ -31,7 +31,7 @@ namespace moe {
 // lane in the same permuted order of k.  The eight warps take an item each;
 // with fewer items several warps share one and split its K.  Bound by the A
 // rows of a decode batch (every token another adapter) or the x of a prefill
-// chunk.
+// chunk.  8192 tokens of one adapter, K = 2048: 10 us at rank 16, 20 at 64.
 constexpr int kShrinkThreads = 256;
 
 // Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K

@@ -27,7 +27,7 @@
 //               the last step that belong to the next group (a product with
 //               zero would let their infinities and NaN through, so both
 //               operands are cleared)
-//   warps 4-7   epilogue: TMEM -> registers -> shared transpose -> 16-byte
+//   warps 4-11  (weights: 4-7) epilogue: TMEM -> registers -> shared transpose -> 16-byte
 //               stores; two accumulators, so it overlaps the next tile's MMAs
 // Every wait is bounded.
 //
@@ -50,17 +50,19 @@
 
 namespace moe {
 
-constexpr int kGroupedThreads = 256;
+constexpr int kEpiWarps = 8;  // two for each quarter of the TMEM lanes, taking turns at the columns (weights: one, with two buffers)
+constexpr int kGroupedThreads = (4 + kEpiWarps) * 32;
 constexpr int kHalfTile = 128 * 128;            // bytes of one CTA's half of an operand, one K = 64 step
 constexpr int kPanel = 64 * 128;                // MN-major: 64 contraction rows x 64 values
 constexpr int kRowPitch = 36;                   // floats: fp32 rows of 32 features, padded
-constexpr int kEpiWarpBytes = 2 * 16 * kRowPitch * 4;  // epilogue transpose buffers of one warp
+constexpr int kEpiWarpBytes = 2560;             // epilogue transpose buffer of one warp (16 fp32 rows, or 2 KB)
+static_assert(16 * kRowPitch * 4 <= kEpiWarpBytes && kEpiWarpBytes % 512 == 0, "buffer; tile stores need 512-byte starts");
 // Ring of (A half, B half): six steps of 256-row tiles, or nine of tiles of at
 // most 64 rows, whose B half is a quarter: where groups are that small reading
 // the matrices is the cost, and three more steps in flight cover HBM's latency.
 constexpr int grouped_stage(bool small) { return kHalfTile + (small ? kHalfTile / 4 : kHalfTile); }
 constexpr int grouped_stages(bool small) { return small ? 9 : 6; }
-constexpr int grouped_smem(bool small) { return grouped_stages(small) * grouped_stage(small) + 4 * kEpiWarpBytes + 1024; }
+constexpr int grouped_smem(bool small) { return grouped_stages(small) * grouped_stage(small) + kEpiWarps * kEpiWarpBytes + 1024; }
 constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
 // 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
@@ -227,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accf_bar[i], 1);
-            mbar_init(&acce_bar[i], 8);
+            mbar_init(&acce_bar[i], 2 * (WG ? 4 : kEpiWarps));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -504,10 +506,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             __syncwarp();
             if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&full_bar[st], 0), 2);  // for both loaders
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && (!WG || warp < 8)) {
         // ======================= epilogue: lane = feature, register = column
-        const int q = warp & 3;
-        uint8_t* stg = smem + kGroupedStages * kGroupedStage + q * kEpiWarpBytes;
+        const int q = warp & 3, turn = (warp - 4) >> 2;
+        uint8_t* stg = smem + kGroupedStages * kGroupedStage + (warp - 4) * (WG ? 2 : 1) * kEpiWarpBytes;
         const bool one = tc::elect_one();
         bool ok = true;
         int it = 0;
@@ -543,19 +545,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     // stmatrix: this lane's row of matrix lane / 8: token, 16-byte piece
                     const int mrow = (lane & 7) + 8 * (lane >> 4), mpiece = (lane >> 3) & 1;
                     uint32_t r[2][16];  // [16 features][fragment of 8 rows]
-                    tc::ld_frags_nowait(tb, r[0]);
-                    tc::ld_frags_nowait(tb + (16u << 16), r[1]);
-                    tc::ld_wait();
-                    for (int c0 = 0; c0 < tl.n; c0 += 32) {
+                    if (32 * turn < tl.n) {
+                        tc::ld_frags_nowait(tb + 32 * turn, r[0]);
+                        tc::ld_frags_nowait(tb + (16u << 16) + 32 * turn, r[1]);
+                        tc::ld_wait();
+                    }
+                    for (int c0 = 32 * turn; c0 < tl.n; c0 += 64) {
                         if constexpr (ADAPT) {
                             if (by_hand && part == 0)
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
                                     if (c0 + 16 * h < tl.n) {
                                         const int t0 = tl.row0 + c0 + 16 * h, left = tl.n - c0 - 16 * h;
-                                        const int m = min(16, left), mn = min(16, left - 16);
-                                        if (bf16) add_delta<true, kTerms>(ex.args, t0, m, t0 + 16, mn, f, &r[0][8 * h], &r[1][8 * h]);
-                                        else add_delta<false, 2>(ex.args, t0, m, t0 + 16, mn, f, &r[0][8 * h], &r[1][8 * h]);
+                                        const int skip = h ? 48 : 16;  // to the warp's next 16 rows
+                                        const int m = min(16, left), mn = min(16, left - skip);
+                                        if (bf16) add_delta<true, kTerms>(ex.args, t0, m, t0 + skip, mn, f, &r[0][8 * h], &r[1][8 * h]);
+                                        else add_delta<false, 2>(ex.args, t0, m, t0 + skip, mn, f, &r[0][8 * h], &r[1][8 * h]);
                                     }
                         }
                         if (ADAPT && !OUT32 && g.accumulate) {  // y's values, added before the one rounding
@@ -573,16 +578,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                                     }
                                 }
                         }
-                        const bool more = c0 + 32 < tl.n;
+                        const bool more = c0 + 64 < tl.n;
                         if (OUT32) {
-                            // 16 rows at a time through two buffers (rows of 32 features, padded against bank
+                            // 16 rows at a time through shared memory (rows of 32 features, padded against bank
                             // conflicts), 16 bytes a lane.  Later parts are added in L2, no old value is waited
                             // for: one lane owns an address, so its additions keep their order
                             const int fr = lane >> 3, fs = (lane & 7) * 4;
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 if (c0 + 16 * h >= tl.n) break;
-                                float* buf = reinterpret_cast<float*>(stg) + h * 16 * kRowPitch;
+                                float* buf = reinterpret_cast<float*>(stg);
+                                __syncwarp();  // the last 16 rows have been read
 #pragma unroll
                                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -602,12 +608,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                                 }
                             }
                             if (more) {
-                                tc::ld_frags_nowait(tb + c0 + 32, r[0]);
-                                tc::ld_frags_nowait(tb + (16u << 16) + c0 + 32, r[1]);
+                                tc::ld_frags_nowait(tb + c0 + 64, r[0]);
+                                tc::ld_frags_nowait(tb + (16u << 16) + c0 + 64, r[1]);
                                 tc::ld_wait();
                             }
                         } else {
-                            uint8_t* buf = stg + ((c0 >> 5) & 1) * 2048;
+                            uint8_t* buf = stg;
+                            __syncwarp();  // the last 32 rows have been read
 #pragma unroll
                             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -621,8 +628,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                                                         pack16(__uint_as_float(v[6]), __uint_as_float(v[7]), bf16));
                                 }
                             if (more) {  // in flight while this block leaves
-                                tc::ld_frags_nowait(tb + c0 + 32, r[0]);
-                                tc::ld_frags_nowait(tb + (16u << 16) + c0 + 32, r[1]);
+                                tc::ld_frags_nowait(tb + c0 + 64, r[0]);
+                                tc::ld_frags_nowait(tb + (16u << 16) + c0 + 64, r[1]);
                             }
                             __syncwarp();
                             uint16_t* out = static_cast<uint16_t*>(g.out) + at + seg * 8;
@@ -656,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         };
                         if (!empty) load(0);
                         for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
-                            uint8_t* buf = stg + ((c0 / kCols) & 1) * 2048;
+                            uint8_t* buf = stg + ((c0 / kCols) & 1) * kEpiWarpBytes;
                             if (one) tc::store_wait_read<1>();
                             if (!empty) tc::ld_wait();
                             __syncwarp();

@@ -31,16 +31,24 @@ namespace moe {
 // lane in the same permuted order of k.  The eight warps take an item each;
 // with fewer items several warps share one and split its K.  Bound by the A
 // rows of a decode batch (every token another adapter) or the x of a prefill
-// chunk.  8192 tokens of one adapter, K = 2048: 10 us at rank 16, 20 at 64.
+// chunk.  8192 tokens of eight requests, K = 2048, x from HBM (5.1 us of it), with
+// an expand_kernel of 8 features behind it: 13 us at rank 16, 15 at 32, 24 at 64.
 constexpr int kShrinkThreads = 256;
 
 // Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K
-// whose operands are in registers at once: as many as about 50 registers hold.
+// in flight.  Large windows keep theirs in a ring in shared memory, as many as leave
+// room for two CTAs an SM (8192 tokens of rank 32 and K = 2048, x from HBM: 15.1 us with
+// the ring, 16.1 with registers; of mixed adapters 46 against 72); small ones hold them
+// in registers, as many as about 50 hold (512 tokens of 30 adapters beside a
+// projection: 36 us, 40 with a ring).
 template <int WIN, int TILES>
 struct ShrinkCfg {
     static constexpr int kOctets = WIN / 8, kTiles = TILES, kRows = 16 * TILES, kPitch = kRows + 4;
-    static constexpr int kVecs = kOctets + 2 * TILES, kSteps = 4 * kVecs <= 12 ? 4 : 2;
-    static constexpr int kRed = 8 * WIN * kPitch * 4;  // bytes: [warp][token of its item][row]
+    static constexpr int kVecs = kOctets + 2 * TILES, kDepth = WIN == 8 ? (kVecs <= 3 ? 4 : 2) : 27 / kVecs;
+    static constexpr int kStep = kVecs * 512;  // bytes of a warp's step
+    static constexpr int kRing = WIN == 8 ? 0 : 8 * kDepth * kStep;
+    static constexpr int kRed = 8 * WIN * kPitch * 4;            // [warp][token of its item][row], in the ring's place
+    static constexpr int kShared = kRing > kRed ? kRing : kRed;  // bytes
 };
 
 template <bool BF16, int WIN, int TERMS, int TILES>
@@ -48,7 +56,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
     using C = ShrinkCfg<WIN, TILES>;
     extern __shared__ __align__(16) uint8_t shrink_smem[];
     float* red = reinterpret_cast<float*>(shrink_smem);                 // [8][WIN][kPitch]
-    float* sums = reinterpret_cast<float*>(shrink_smem + C::kRed);      // [WIN][r]
+    float* sums = reinterpret_cast<float*>(shrink_smem + C::kShared);   // [WIN][r]
     __shared__ int item_adapter[WIN], item_count[WIN];
     __shared__ int8_t item_tok[WIN][WIN];          // tokens of an item, in order
     __shared__ int8_t tok_item[WIN], tok_place[WIN];  // a token's item (-1: none) and place in it
@@ -101,49 +109,76 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
 #pragma unroll
                 for (int q = 0; q < 2 * C::kTiles; ++q)
                     ar[q] = A + ((int64_t)a * p.r + j0 + (q * 8 + gq < rows ? q * 8 + gq : gq)) * p.K + 8 * c;
-                // a step's operands load kSteps - 1 steps before it is multiplied; only a last, partial step
-                // looks at the end of K
-                uint4 bv[C::kSteps][C::kOctets], av[C::kSteps][2 * C::kTiles];
-                auto load = [&](int b, int k) {
-                    if (k + 32 <= ke) {
+                auto multiply = [&](auto operand) {
+                    uint4 bv[C::kOctets];
 #pragma unroll
-                        for (int o = 0; o < C::kOctets; ++o) bv[b][o] = __ldg(reinterpret_cast<const uint4*>(xr[o] + k));
-#pragma unroll
-                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = __ldg(reinterpret_cast<const uint4*>(ar[q] + k));
-                    } else {
-                        const bool in = k + 8 * c < ke;
-#pragma unroll
-                        for (int o = 0; o < C::kOctets; ++o) bv[b][o] = load_or_zero(xr[o] + k, in);
-#pragma unroll
-                        for (int q = 0; q < 2 * C::kTiles; ++q) av[b][q] = load_or_zero(ar[q] + k, in);
-                    }
-                };
-                auto multiply = [&](int b) {
+                    for (int o = 0; o < C::kOctets; ++o)
+                        if (o == 0 || o < octets) bv[o] = operand(o);
 #pragma unroll
                     for (int q = 0; q < C::kTiles; ++q) {
-                        const uint4 lo = av[b][2 * q], hi = av[b][2 * q + 1];
+                        const uint4 lo = operand(C::kOctets + 2 * q), hi = operand(C::kOctets + 2 * q + 1);
                         const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
                         for (int o = 0; o < C::kOctets; ++o) {
-                            if (o > 0 && octets == 1) break;
-                            mma16<BF16>(acc[q][o], f0, bv[b][o].x, bv[b][o].y);
-                            mma16<BF16>(acc[q][o], f1, bv[b][o].z, bv[b][o].w);
+                            if (o > 0 && o >= octets) break;
+                            mma16<BF16>(acc[q][o], f0, bv[o].x, bv[o].y);
+                            mma16<BF16>(acc[q][o], f1, bv[o].z, bv[o].w);
                         }
                     }
                 };
+                auto source = [&](int v) { return v < C::kOctets ? xr[v] : ar[v - C::kOctets]; };
+                if constexpr (C::kRing > 0) {
+                    // a lane copies what it will multiply itself: the ring needs no barrier
+                    uint8_t* ring = shrink_smem + warp * C::kDepth * C::kStep + lane * 16;
+                    auto fetch = [&](uint8_t* to, int k) {
+                        const uint32_t bytes = k + 8 * c < ke ? 16 : 0;
 #pragma unroll
-                for (int b = 0; b < C::kSteps - 1; ++b)
-                    if (kb + 32 * b < ke) load(b, kb + 32 * b);
-                for (int k0 = kb; k0 < ke; k0 += 32 * C::kSteps) {
+                        for (int v = 0; v < C::kVecs; ++v)
+                            if (v < octets || v >= C::kOctets) tc::cp16_or_zero(to + v * 512, source(v) + k, bytes);
+                    };
 #pragma unroll
-                    for (int b = 0; b < C::kSteps; ++b) {
-                        const int k = k0 + 32 * b, ahead = k + 32 * (C::kSteps - 1);
-                        if (ahead < ke) load((b + C::kSteps - 1) % C::kSteps, ahead);
-                        if (k < ke) multiply(b);
+                    for (int b = 0; b < C::kDepth - 1; ++b) {
+                        if (kb + 32 * b < ke) fetch(ring + b * C::kStep, kb + 32 * b);
+                        tc::cp_commit();
+                    }
+                    int in = C::kDepth - 1, out = 0;  // the ring's places to fill and to read
+                    for (int k = kb; k < ke; k += 32) {
+                        const int ahead = k + 32 * (C::kDepth - 1);
+                        if (ahead < ke) fetch(ring + in * C::kStep, ahead);
+                        tc::cp_commit();
+                        tc::cp_wait<C::kDepth - 1>();
+                        const uint8_t* from = ring + out * C::kStep;
+                        multiply([&](int v) { return *reinterpret_cast<const uint4*>(from + v * 512); });
+                        in = in + 1 == C::kDepth ? 0 : in + 1;
+                        out = out + 1 == C::kDepth ? 0 : out + 1;
+                    }
+                } else {
+                    // (only a last, partial step looks at the end of K)
+                    uint4 held[C::kDepth][C::kVecs];
+                    auto fetch = [&](int b, int k) {
+                        if (k + 32 <= ke) {
+#pragma unroll
+                            for (int v = 0; v < C::kVecs; ++v) held[b][v] = __ldg(reinterpret_cast<const uint4*>(source(v) + k));
+                        } else {
+                            const bool in = k + 8 * c < ke;
+#pragma unroll
+                            for (int v = 0; v < C::kVecs; ++v) held[b][v] = load_or_zero(source(v) + k, in);
+                        }
+                    };
+#pragma unroll
+                    for (int b = 0; b < C::kDepth - 1; ++b)
+                        if (kb + 32 * b < ke) fetch(b, kb + 32 * b);
+                    for (int k0 = kb; k0 < ke; k0 += 32 * C::kDepth) {
+#pragma unroll
+                        for (int b = 0; b < C::kDepth; ++b) {
+                            const int k = k0 + 32 * b, ahead = k + 32 * (C::kDepth - 1);
+                            if (ahead < ke) fetch((b + C::kDepth - 1) % C::kDepth, ahead);
+                            if (k < ke) multiply([&](int v) { return held[b][v]; });
+                        }
                     }
                 }
             }
-            __syncthreads();  // the last pass's sums have been read
+            __syncthreads();  // every warp is through with its ring, or the last pass's sums
             float* mr = red + warp * WIN * C::kPitch;
 #pragma unroll
             for (int q = 0; q < C::kTiles; ++q)
@@ -169,6 +204,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                     if (q < share) s += src[q * WIN * C::kPitch];
                 sums[m * p.r + j0 + j] = s;
             }
+            if (C::kRing > 0 && (j0 + C::kRows < p.r || base + at_once < items)) __syncthreads();  // the next pass fills the ring
         }
     }
     if (p.slices > 1) tc::cluster_sync();
@@ -336,7 +372,8 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
 constexpr int kSmallWindowTokens = 148 * 8;
 
 // CTAs that split a window's K: a power of two up to 8, so that the windows'
-// CTAs fill the GPU once while each keeps at least 256 of K.
+// CTAs fill the GPU once while each keeps at least 256 of K (as many as run two an
+// SM, powers of two or not: 1500 tokens of rank 16, K = 2048, 13.8 us against 9.5).
 static int shrink_slices(int T, int K) {
     const int win = T <= kSmallWindowTokens ? 8 : 32, windows = (T + win - 1) / win;
     int s = 1;
@@ -352,7 +389,7 @@ size_t adapter_workspace(int T, int r) {
 template <bool BF16, int WIN, int TERMS, int TILES>
 static cudaError_t shrink_tiles(const AdapterArgs& p, cudaStream_t s) {
     auto kern = shrink_kernel<BF16, WIN, TERMS, TILES>;
-    const int smem = ShrinkCfg<WIN, TILES>::kRed + WIN * p.r * 4;
+    const int smem = ShrinkCfg<WIN, TILES>::kShared + WIN * p.r * 4;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;

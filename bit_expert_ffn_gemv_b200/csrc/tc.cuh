@@ -88,6 +88,10 @@ MOE_DEV void cp8(void* dst, const void* src) {
 MOE_DEV void cp4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
+// (bytes 0: zeros, and the source is not read)
+MOE_DEV void cp16_or_zero(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
 MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 MOE_DEV void cp_wait() {

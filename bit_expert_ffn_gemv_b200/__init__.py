@@ -336,15 +336,12 @@ class MoeLayer:
         from .experts16 import adapter_project
         if y is not None and y.data_ptr() == x.data_ptr() and not flags & MOE_NORM_INPUT:
             raise ValueError("y == x: the adapters read x after the layer has updated it (use MOE_NORM_INPUT)")
-        u = x
-        if flags & MOE_NORM_INPUT:
-            with torch.cuda.device(x.device):
-                u = rms_normalize(x, stream=stream)
-            if stream is not None:
-                u.record_stream(stream)  # freed on return, possibly before the calls below have run
-        y = self.forward(layer, u, y, flags & ~MOE_NORM_INPUT, stream)
-        return adapter_project(u, a, b, ids, scale=scale, out=y, flags=MOE_ACCUMULATE | (flags & MOE_OUT_FP32),
-                               stream=stream)
+        # (on the stream: what is allocated here is freed, or handed out, before the calls have run)
+        with torch.cuda.device(x.device), torch.cuda.stream(stream):
+            u = rms_normalize(x, stream=stream) if flags & MOE_NORM_INPUT else x
+            y = self.forward(layer, u, y, flags & ~MOE_NORM_INPUT, stream)
+            return adapter_project(u, a, b, ids, scale=scale, out=y, flags=MOE_ACCUMULATE | (flags & MOE_OUT_FP32),
+                                   stream=stream)
 
     def forward_host(self, layer, x_host, y_host, flags=0, stream=None):
         moe_forward_host(self.handle, layer, x_host.data_ptr(), x_host.shape[0], y_host.data_ptr(), flags,

@@ -78,7 +78,7 @@ moe_status moe_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_
         if (acc) return MOE_OK;
         return cuda_status(cudaMemsetAsync(dw, 0, (size_t)n_groups * n * k * (f32 ? 4 : 2), s));
     }
-    if (!good(dy) || !good(x) || !offsets || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
+    if (!good(dy) || !good(x) || dw == dy || dw == x || !offsets || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
     moe::GroupedArgs g{};
     g.offsets = offsets;
     g.E = n_groups;

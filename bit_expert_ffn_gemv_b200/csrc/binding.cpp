@@ -140,15 +140,46 @@ ScalarType result_type(PyObject* out, PyObject* out_dtype, ScalarType type) {
     return t;
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v == 1;
+}
 uint32_t type_flag(ScalarType t) { return t == ScalarType::Half ? MOE_OP_FP16 : 0u; }
 uint32_t fp32_flag(ScalarType t) { return t == ScalarType::Float ? MOE_OUT_FP32 : 0u; }
 
-// the stream a call is enqueued on: a cudaStream_t as an integer, or (None) the device's current one
-void* stream_of(PyObject* o, int dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-    return PyLong_AsVoidPtr(o);
-}
+// The device and stream of a call: the given torch.cuda.Stream, or (None) the
+// device's current one.  What the call allocates belongs to that stream: memory of
+// another stream's pool may still be in use there, and the workspace is freed on
+// return, before the call has run.
+class Call {
+    c10::cuda::CUDAGuard device_;
+    std::optional<c10::cuda::CUDAStreamGuard> given_;
+
+    static PyObject* attribute(PyObject* o, const char* name) {
+        PyObject* v = PyObject_GetAttrString(o, name);
+        if (!v) throw python_error();
+        return v;
+    }
+
+public:
+    void* stream;
+    Call(PyObject* o, int dev) : device_((c10::DeviceIndex)dev) {
+        if (o == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+            return;
+        }
+        PyObject* v = attribute(o, "device_index");
+        const long on = PyLong_AsLong(v);
+        Py_DECREF(v);
+        v = attribute(o, "cuda_stream");
+        stream = PyLong_AsVoidPtr(v);
+        Py_DECREF(v);
+        if (PyErr_Occurred()) throw python_error();
+        TORCH_CHECK_VALUE(on == dev, "stream: one of cuda:", dev, " is expected, not of cuda:", on);
+        given_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)dev));
+    }
+};
 
 void arguments(Py_ssize_t got, Py_ssize_t want) { TORCH_CHECK_TYPE(got == want, want, " arguments are expected, not ", got); }
 
@@ -167,14 +198,14 @@ PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const void* off = vector(a[2], "offsets", x.dev, ScalarType::Int, E + 1);
     const int64_t cols = tr ? k : n;
     const ScalarType type = result_type(a[3], a[5], x.type);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.dev);
+    const Call call(a[6], x.dev);
     Result y = result(a[3], "out", {x.rows, cols}, x.t, type);
     const int64_t ldy = matrix(of(y), "out", x.dev, type, x.rows, cols);
     const moe_status s = moe_grouped_matmul(x.t.data_ptr(), x.ld, int32(x.rows, "rows"), w.data_ptr(),
                                             static_cast<const int32_t*>(off), int32(E, "E"), int32(n, "n"), int32(k, "k"),
                                             of(y).data_ptr(), ldy,
                                             type_flag(x.type) | fp32_flag(type) | (tr ? MOE_OP_TRANSPOSE : 0u),
-                                            stream_of(a[6], x.dev));
+                                            call.stream);
     if (s != MOE_OK) return raise_status(s, "moe_grouped_matmul");
     return y.object();
     END_HANDLE_TH_ERRORS
@@ -194,14 +225,14 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const bool add = truth(a[5]);
     TORCH_CHECK_VALUE(!add || a[3] != Py_None, "accumulate adds to a given out");
     const ScalarType type = result_type(a[3], a[4], dy.type);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dy.dev);
+    const Call call(a[6], dy.dev);
     Result dw = result(a[3], "out", {E, n, k}, dy.t, type);
     block(of(dw), "out", dy.dev, type, {E, n, k});
     const moe_status s = moe_grouped_wgrad(dy.t.data_ptr(), dy.ld, x.data_ptr(), ldx, int32(dy.rows, "rows"),
                                            static_cast<const int32_t*>(off), int32(E, "E"), int32(n, "n"), int32(k, "k"),
                                            of(dw).data_ptr(),
                                            type_flag(dy.type) | fp32_flag(type) | (add ? MOE_ACCUMULATE : 0u),
-                                           stream_of(a[6], dy.dev));
+                                           call.stream);
     if (s != MOE_OK) return raise_status(s, "moe_grouped_wgrad");
     return dw.object();
     END_HANDLE_TH_ERRORS
@@ -220,12 +251,12 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const int64_t f = half_cols(gu);
     const void* rw = vector(a[1], "row_weights", gu.dev, ScalarType::Float, gu.rows);
     const void* nr = vector(a[3], "n_rows", gu.dev, ScalarType::Int, 1);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)gu.dev);
+    const Call call(a[4], gu.dev);
     Result h = result(a[2], "out", {gu.rows, f}, gu.t, gu.type);
     const int64_t ldh = matrix(of(h), "out", gu.dev, gu.type, gu.rows, f);
     const moe_status s = moe_swiglu(gu.t.data_ptr(), gu.ld, int32(gu.rows, "rows"), int32(f, "f"),
                                     static_cast<const float*>(rw), static_cast<const int32_t*>(nr), of(h).data_ptr(), ldh,
-                                    type_flag(gu.type), stream_of(a[4], gu.dev));
+                                    type_flag(gu.type), call.stream);
     if (s != MOE_OK) return raise_status(s, "moe_swiglu");
     return h.object();
     END_HANDLE_TH_ERRORS
@@ -243,7 +274,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     TORCH_CHECK_VALUE(weighted || a[5] == Py_None, "drw: needs row_weights");
     const void* rw = vector(a[2], "row_weights", gu.dev, ScalarType::Float, gu.rows);
     const void* nr = vector(a[7], "n_rows", gu.dev, ScalarType::Int, 1);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)gu.dev);
+    const Call call(a[8], gu.dev);
     Result dgu = result(a[3], "dgu", {gu.rows, 2 * f}, gu.t, gu.type), h, drw;
     const int64_t lddgu = matrix(of(dgu), "dgu", gu.dev, gu.type, gu.rows, 2 * f);
     int64_t ldh = 0;
@@ -260,7 +291,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const moe_status s = moe_swiglu_backward(gu.t.data_ptr(), gu.ld, dh.data_ptr(), lddh, int32(gu.rows, "rows"),
                                              int32(f, "f"), static_cast<const float*>(rw), static_cast<const int32_t*>(nr),
                                              of(dgu).data_ptr(), lddgu, want_h ? of(h).data_ptr() : nullptr, ldh, dw,
-                                             type_flag(gu.type), stream_of(a[8], gu.dev));
+                                             type_flag(gu.type), call.stream);
     if (s != MOE_OK) return raise_status(s, "moe_swiglu_backward");
     PyObject *o1 = dgu.object(), *o2 = want_h ? h.object() : Py_NewRef(Py_None),
              *o3 = weighted ? drw.object() : Py_NewRef(Py_None);
@@ -272,10 +303,10 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     END_HANDLE_TH_ERRORS
 }
 
-// x, a, b, ids, w, scale, out, flags, workspace, stream
+// x, a, b, ids, w, scale, out, flags, stream
 PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
     HANDLE_TH_ERRORS
-    arguments(count, 10);
+    arguments(count, 9);
     const Operand x = operand(a[0], "x");
     const Tensor &A = tensor(a[1], "a"), &B = tensor(a[2], "b");
     TORCH_CHECK_VALUE(A.dim() == 3 && B.dim() == 3, "a, b: contiguous [L, rank, k] and [L, n, rank] tensors are expected");
@@ -295,7 +326,7 @@ PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
     TORCH_CHECK_VALUE(!PyErr_Occurred() && flags <= UINT32_MAX, "flags: a sum of MOE_OUT_FP32 and MOE_ACCUMULATE is expected");
     TORCH_CHECK_VALUE(!(flags & MOE_ACCUMULATE) || a[6] != Py_None, "MOE_ACCUMULATE adds to a given out");
     const ScalarType type = (flags & MOE_OUT_FP32) ? ScalarType::Float : x.type;
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.dev);
+    const Call call(a[8], x.dev);
     Result y = result(a[6], "out", {x.rows, n}, x.t, type);
     p.ldy = matrix(of(y), "out", x.dev, type, x.rows, n);
     p.x = x.t.data_ptr();
@@ -308,18 +339,10 @@ PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
     p.n_adapters = int32(L, "L");
     p.rank = int32(rank, "rank");
     p.y = of(y).data_ptr();
-    // freed when this call returns: the caching allocator gives it to later work of the same stream only
-    Tensor made;
     p.workspace_bytes = moe_adapter_workspace(p.tokens, p.rank);
-    if (a[8] != Py_None) {
-        const Tensor& ws = tensor(a[8], "workspace");
-        on_device(ws, "workspace", x.dev);
-        p.workspace = ws.data_ptr();
-    } else {
-        made = at::empty({(int64_t)p.workspace_bytes}, x.t.options().dtype(ScalarType::Byte));
-        p.workspace = made.data_ptr();
-    }
-    const moe_status s = moe_adapter_project(&p, (uint32_t)flags | type_flag(x.type), stream_of(a[9], x.dev));
+    const Tensor workspace = at::empty({(int64_t)p.workspace_bytes}, x.t.options().dtype(ScalarType::Byte));
+    p.workspace = workspace.data_ptr();
+    const moe_status s = moe_adapter_project(&p, (uint32_t)flags | type_flag(x.type), call.stream);
     if (s != MOE_OK) return raise_status(s, "moe_adapter_project");
     return y.object();
     END_HANDLE_TH_ERRORS

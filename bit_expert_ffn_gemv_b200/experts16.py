@@ -3,8 +3,9 @@
 Wrappers of the C calls (moe_grouped_matmul, moe_grouped_wgrad, moe_swiglu, moe_swiglu_backward and
 moe_adapter_project in include/moe.h).  The checks of types, shapes and strides, the results' allocation and the call
 are in csrc/binding.cpp (module _ops16): ValueError for tensors that do not fit, MoeError for what the library
-refuses.  Work is enqueued on ``stream`` (a torch.cuda.Stream; default: the current stream of the tensors' device).
-No call synchronises.  There is no autograd: the gradients are calls of their own.
+refuses.  Work is enqueued on ``stream`` (a torch.cuda.Stream; default: the current stream of the tensors' device),
+and a result that is not given is allocated for that stream.  No call synchronises.  There is no autograd: the
+gradients are calls of their own.
 
 Rows are (token, expert) pairs sorted by expert; ``offsets`` (int32 [E + 1], on the device) gives each expert's row
 range.  An expert FFN and its gradient, for gate/up matrices w1 [E, 2f, d] and down matrices w2 [E, d, f]:
@@ -23,8 +24,6 @@ Rows outside every group are left as they were in a given ``out``, and are unset
 """
 from __future__ import annotations
 
-import torch
-
 from . import MoeError, lib
 
 lib()  # libmoe.so, which the binding links against; raises with the build's command if it is absent
@@ -40,35 +39,29 @@ __all__ = ["grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward"
 def grouped_matmul(x, w, offsets, out=None, transpose=False, out_dtype=None, stream=None):
     """x [rows, k] times each group's W_e^T -> [rows, n]; w [E, n, k] contiguous.  With transpose: x [rows, n] times
     W_e -> [rows, k].  out (or out_dtype): x's type or fp32."""
-    return _ops16.grouped_matmul(x, w, offsets, out, transpose, out_dtype, stream if stream is None else stream.cuda_stream)
+    return _ops16.grouped_matmul(x, w, offsets, out, transpose, out_dtype, stream)
 
 
 def grouped_matmul_wgrad(dy, x, offsets, out=None, out_dtype=None, accumulate=False, stream=None):
     """dy_e^T x_e of each group: dy [rows, n], x [rows, k] -> [E, n, k] of dy's type or fp32; accumulate adds to an
     fp32 out."""
-    return _ops16.grouped_wgrad(dy, x, offsets, out, out_dtype, accumulate, stream if stream is None else stream.cuda_stream)
+    return _ops16.grouped_wgrad(dy, x, offsets, out, out_dtype, accumulate, stream)
 
 
 def swiglu(gu, row_weights=None, out=None, n_rows=None, stream=None):
     """row_weights * silu(g) * u for gu = [g | u] [rows, 2f] -> [rows, f].  n_rows: int32 device tensor of one value,
     rows from it on are left as they were."""
-    return _ops16.swiglu(gu, row_weights, out, n_rows, stream if stream is None else stream.cuda_stream)
+    return _ops16.swiglu(gu, row_weights, out, n_rows, stream)
 
 
 def swiglu_backward(gu, dh, row_weights=None, dgu=None, h=None, drw=None, with_h=False, n_rows=None, stream=None):
     """Gradient of swiglu: (dgu [rows, 2f], h or None, d_row_weights or None).  h, the forward's result again, is
     written when given or with_h; d_row_weights when row_weights is given."""
-    return _ops16.swiglu_backward(gu, dh, row_weights, dgu, h, drw, with_h, n_rows,
-                                  stream if stream is None else stream.cuda_stream)
+    return _ops16.swiglu_backward(gu, dh, row_weights, dgu, h, drw, with_h, n_rows, stream)
 
 
 def adapter_project(x, a, b, ids, w=None, scale=None, out=None, flags=0, stream=None):
     """[w x_t +] scale[i] * b[i] (a[i] x_t) for every token t with its adapter i = ids[t]: x [T, k], a [L, rank, k],
     b [L, n, rank], ids int32 [T], w [n, k], scale fp32 [L] -> [T, n], x's type, or fp32 with MOE_OUT_FP32 in flags.
     With MOE_ACCUMULATE the result is added to out.  An id outside [0, L): no adapter."""
-    if stream is None:
-        return _ops16.adapter_project(x, a, b, ids, w, scale, out, flags, None, None)
-    # the workspace is freed on return, possibly before the call has run on its stream
-    ws = torch.empty(lib().moe_adapter_workspace(x.shape[0], a.shape[1]), dtype=torch.uint8, device=x.device)
-    ws.record_stream(stream)
-    return _ops16.adapter_project(x, a, b, ids, w, scale, out, flags, ws, stream.cuda_stream)
+    return _ops16.adapter_project(x, a, b, ids, w, scale, out, flags, stream)

@@ -412,6 +412,7 @@ const char* moe_kernel_name(int32_t kernel);
  *     ranges; rows before offsets[0] and from offsets[n_groups] on belong to
  *     no group: they are not read into any result, and their result rows are
  *     left as they were.  Values are clamped to [0, rows].
+ *   - Results overlap no operand.
  *   - rows = 0 is valid.  A device-side wait that ran out surfaces through
  *     moe_check_op_status.
  */

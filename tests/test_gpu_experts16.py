@@ -303,3 +303,46 @@ def test_back_to_back_calls_are_ordered(rows):
     for _ in range(4):
         for p, q in zip(plain, chain(False)):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("op", ["grouped_matmul", "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "adapter_project",
+                                "forward_adapted"])
+def test_a_result_allocated_for_a_given_stream(op):
+    """A result that a call on another stream allocates is no block that the caller's stream still writes."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rnd = lambda *shape: torch.randn(*shape, generator=g, device="cuda").bfloat16()
+    sh = MoeShape(d=256, f=128, E=16, k=2, n_shared=0, bits=2)
+    h, x = _layer(sh, 64)
+    try:
+        rows, E = 64, 4
+        off = torch.arange(0, rows + 1, rows // E, device="cuda").int()
+        w, gu, dy = rnd(E, 256, sh.d), rnd(rows, 512), rnd(rows, 256)
+        a, b, ids = rnd(3, 8, sh.d), rnd(3, sh.d, 8), torch.arange(rows, device="cuda").int() % 3
+        call = {"grouped_matmul": lambda s: moe.grouped_matmul(x, w, off, stream=s),
+                "grouped_matmul_wgrad": lambda s: moe.grouped_matmul_wgrad(dy, x, off, stream=s),
+                "swiglu": lambda s: moe.swiglu(gu, stream=s),
+                "swiglu_backward": lambda s: moe.swiglu_backward(gu, dy, stream=s)[0],
+                "adapter_project": lambda s: moe.adapter_project(x, a, b, ids, stream=s),
+                "forward_adapted": lambda s: h.forward_adapted(0, x, a, b, ids, flags=moe.MOE_NORM_INPUT, stream=s)}[op]
+        ref = call(None).clone()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        torch.cuda._sleep(50_000_000)  # the caller's stream is busy for some 25 ms
+        busy = [torch.empty_like(ref).fill_(7) for _ in range(8)]  # written after that
+        del busy
+        got = call(s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+    finally:
+        h.close()
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Other:  # (what the wrappers read of a torch.cuda.Stream)
+        device_index, cuda_stream = torch.cuda.current_device() + 1, 0
+
+    gu = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        moe.swiglu(gu, stream=Other())
+    with pytest.raises(AttributeError):
+        moe.swiglu(gu, stream=3)

@@ -33,12 +33,13 @@ def test_grouped_matmul(L, bad):
                                 a["ldy"], a["flags"], None) == 1
 
 
-GOOD_WGRAD = dict(dy=P, lddy=32, x=P, ldx=64, rows=10, offsets=P, groups=4, n=32, k=64, dw=P, flags=0)
+GOOD_WGRAD = dict(dy=P, lddy=32, x=3 * P, ldx=64, rows=10, offsets=P, groups=4, n=32, k=64, dw=2 * P, flags=0)
 
 
 @pytest.mark.parametrize("bad", [
     dict(rows=-1), dict(groups=0), dict(groups=2000), dict(n=9), dict(k=0), dict(lddy=31), dict(ldx=8), dict(dy=0),
-    dict(dy=P + 8), dict(x=0), dict(x=P + 1), dict(offsets=0), dict(dw=0), dict(dw=P + 8), dict(flags=0x2),  # accumulate into 16 bits
+    dict(dy=P + 8), dict(x=0), dict(x=P + 1), dict(offsets=0), dict(dw=0), dict(dw=P + 8), dict(dw=P), dict(dw=3 * P),
+    dict(flags=0x2),  # accumulate into 16 bits
     dict(flags=0x200), dict(flags=0x40)], ids=str)
 def test_grouped_wgrad(L, bad):
     a = dict(GOOD_WGRAD, **bad)

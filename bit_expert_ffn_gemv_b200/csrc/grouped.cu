@@ -830,7 +830,7 @@ cudaError_t launch_grouped(int mode, const GroupedArgs& args, const void* w, con
     }
     const bool forward = mode == kGroupedForward;
     // Few rows: the warp-MMA kernel while the tiles would not give every pair of SMs one, which costs the
-    // tensor-core kernel its start-up and leaves SMs idle (64 rows of one 2048 x 2048 matrix: 8.2 us against
+    // tensor-core kernel its start-up and leaves SMs idle (64 rows of one 2048 x 2048 matrix: 6.9 us against
     // 12.5; of 64 such matrices: 78 us against 58, its CTAs living too short for HBM).
     if (forward && g.M <= kSkinnyMaxRows && (g.E < g.M ? g.E : g.M) * JT < sm_count() / 2)
         return launch_skinny_grouped(g, w, x, ldx, out_fp32, s);

@@ -8,7 +8,7 @@
 // computed.  The warps' sums meet in shared memory in warp order
 // (deterministic).  Bound by HBM, 2 N K bytes per matrix, and by the latency of
 // a CTA's few loads: ten rows of ten 1536 x 2048 matrices take 13.5 us, 71% of
-// the measured copy; one row-block of 64 rows by 2048 x 2048 8.5 us.
+// the measured copy; one row-block of 64 rows by 2048 x 2048 6.9 us.
 //
 // Grouped form: a CTA finds the group it works for in the offsets (one round of
 // loads and a prefix count of those that hold rows), so no list of groups is
@@ -96,9 +96,11 @@ MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t*
     }
 }
 
-// MAXNB: blocks of 8 rows that a group can have (the call's rows, rounded up)
-template <bool BF16, bool OUT32, bool ADAPT, int MAXNB>
-__global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyArgs p) {
+// MAXNB: blocks of 8 rows that a group can have (the call's rows, rounded up).
+// PER_SM: CTAs an SM must hold; one, where there is no second, leaves registers
+// for all of x's loads in flight.
+template <bool BF16, bool OUT32, bool ADAPT, int MAXNB, int PER_SM = 2>
+__global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const SkinnyArgs p) {
     constexpr int kPitch = 8 * MAXNB + 1;
     __shared__ __align__(16) float red[8][16 * kPitch];
     __shared__ int found[3], counts[8];
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2) skinny_kernel(const SkinnyA
     if (n <= 8) skinny_sums<BF16, 1>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     else if (MAXNB == 2 || (MAXNB > 2 && n <= 16)) skinny_sums<BF16, 2>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     else if (MAXNB == 8 && n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    // (a decode batch of 48 requests with adapters: 9.9 us, 10.8 as 64 rows; products do not gain)
+    else if (ADAPT && MAXNB == 8 && n <= 48) skinny_sums<BF16, 6>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     else if (MAXNB == 8) skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     __syncthreads();
     grid_release();  // (late: the next kernel's CTAs then spread over the SMs as evenly as this one's)
@@ -234,6 +238,9 @@ static cudaError_t skinny(const SkinnyArgs& p, int rows, dim3 grid, cudaStream_t
     auto kern = rows <= 8    ? skinny_kernel<BF16, OUT32, ADAPT, 1>
                 : rows <= 16 ? skinny_kernel<BF16, OUT32, ADAPT, 2>
                              : skinny_kernel<BF16, OUT32, ADAPT, 8>;
+    // at most a CTA an SM (64 rows of one 2048 x 2048 matrix: 6.9 us against 8.7; of 8 matrices, 18.1 against 14.4)
+    if constexpr (!ADAPT)
+        if (rows > 16 && grid.x * grid.y <= 148) kern = skinny_kernel<BF16, OUT32, false, 8, 1>;
     return launch_behind(kern, grid, kSkinnyThreads, 0, s, p);
 }
 

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 32, 33, 63, 64, 65])
-@pytest.mark.parametrize("E,N,K", [(1, 40, 8), (3, 136, 328), (40, 64, 2056)])
+@pytest.mark.parametrize("E,N,K", [(1, 40, 8), (3, 136, 328), (40, 64, 2056), (2, 1608, 264)])
 @pytest.mark.parametrize("out_dtype", [None, torch.float32])
 def test_few_rows(M, E, N, K, dtype, out_dtype):
     g = torch.Generator(device="cuda").manual_seed(M * 100 + E)

@@ -513,6 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         const bool one = tc::elect_one();
         bool ok = true;
         int it = 0;
+        uint32_t stores = 0;  // weights: tile stores issued; their number, not the column, says whose turn a buffer is
         const bool bf16 = g.bf16 != 0;
         if (ADAPT) grid_wait();  // v, from the kernel before
         for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
@@ -647,7 +648,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     }
                 } else {
                     // 32 features x 64 bytes at a time, through two swizzled buffers and tile stores (which
-                    // clip at the matrix's edges).  Later parts, and MOE_ACCUMULATE, are added in L2 by the
+                    // clip at the matrix's edges).  The buffers take turns across tiles too: after the wait
+                    // for all stores but the last, that last one reads the other buffer, whatever number of
+                    // blocks a tile has.  Later parts, and MOE_ACCUMULATE, are added in L2 by the
                     // store itself, each part once the one before has landed: a fixed order of additions
                     constexpr int kCols = OUT32 ? 16 : 32;
                     if (part > 0) {
@@ -663,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                         };
                         if (!empty) load(0);
                         for (int c0 = 0; c0 < 256 && tl.g0 + c0 < g.C; c0 += kCols) {
-                            uint8_t* buf = stg + ((c0 / kCols) & 1) * kEpiWarpBytes;
+                            uint8_t* buf = stg + (stores++ & 1) * kEpiWarpBytes;
                             if (one) tc::store_wait_read<1>();
                             if (!empty) tc::ld_wait();
                             __syncwarp();

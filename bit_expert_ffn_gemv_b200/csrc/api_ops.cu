@@ -15,7 +15,7 @@ __device__ uint32_t g_op_status;
 
 namespace {
 
-constexpr int kMaxGroups = 1024;
+constexpr int kMaxGroups = moe::kGroupedMaxGroups;
 constexpr int32_t kMaxRows = 1 << 27;  // row blocks of all groups and their tiles stay inside 32 bits
 constexpr int32_t kMaxCols = 1 << 17;
 constexpr int32_t kMaxRank = moe::kMaxAdapterRank;

@@ -63,7 +63,6 @@ static_assert(16 * kRowPitch * 4 <= kEpiWarpBytes && kEpiWarpBytes % 512 == 0, "
 constexpr int grouped_stage(bool small) { return kHalfTile + (small ? kHalfTile / 4 : kHalfTile); }
 constexpr int grouped_stages(bool small) { return small ? 9 : 6; }
 constexpr int grouped_smem(bool small) { return grouped_stages(small) * grouped_stage(small) + kEpiWarps * kEpiWarpBytes + 1024; }
-constexpr int kGroupedMaxGroups = 1024;
 // fp32 results: the tensor core rounds its accumulator towards zero at every
 // 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
 // relative after 1875 steps), so the contraction is cut into parts of this

@@ -168,6 +168,7 @@ cudaError_t launch_dequant(const uint8_t* codes, const uint16_t* scales, int N, 
 
 // ---------------------------------------------------------------- 16-bit experts: grouped products
 // Modes of the grouped product: y = x W^T, dx = dy W, dW = dy^T x.
+constexpr int kGroupedMaxGroups = 1024;
 constexpr int kGroupedForward = 0, kGroupedRows = 1, kGroupedWeights = 2;
 struct GroupedArgs {
     const int32_t* offsets;  // [E + 1] row ranges of the groups

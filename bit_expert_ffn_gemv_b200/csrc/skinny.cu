@@ -109,9 +109,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const Sk
     int e = 0, row0 = 0, n = ADAPT ? p.ad.T : 0;
     if (!ADAPT) {
         // this CTA's group: the blockIdx.y-th that holds rows (a thread looks at up to four)
-        constexpr int kMost = 4;
+        constexpr int kMost = kGroupedMaxGroups / kSkinnyThreads;
         const int each = (p.E + kSkinnyThreads - 1) / kSkinnyThreads, first = tid * each;
         int lo[kMost], hi[kMost], mine = 0;
+        constexpr int kFalls = 1 << 16;  // added, above the counts, where an offset is below the one before it
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
             lo[i] = hi[i] = 0;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const Sk
                 lo[i] = min(max(__ldg(&p.offsets[first + i]), 0), p.M);
                 hi[i] = min(max(__ldg(&p.offsets[first + i + 1]), 0), p.M);
             }
-            mine += hi[i] > lo[i];
+            mine += hi[i] > lo[i] ? 1 : hi[i] < lo[i] ? kFalls : 0;
         }
         int before = mine;
 #pragma unroll
@@ -131,18 +132,36 @@ __global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const Sk
         if (tid == 0) found[1] = -1;
         __syncthreads();
         before -= mine;
+        int all = 0;
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < warp) before += counts[q];
+        for (int q = 0; q < 8; ++q) {
+            const int c = counts[q];
+            if (q < warp) before += c;
+            all += c;
+        }
+        if (all < kFalls) {
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            if (hi[i] <= lo[i]) continue;
-            if (before == (int)blockIdx.y) {
-                found[0] = first + i;
-                found[1] = lo[i];
-                found[2] = hi[i] - lo[i];
+            for (int i = 0; i < kMost; ++i) {
+                if (hi[i] <= lo[i]) continue;
+                if (before == (int)blockIdx.y) {
+                    found[0] = first + i;
+                    found[1] = lo[i];
+                    found[2] = hi[i] - lo[i];
+                }
+                ++before;
             }
-            ++before;
+        } else if (tid == 0) {
+            // made ascending, as in the tensor-core kernel, so that no two groups share a row
+            int at = min(max(__ldg(&p.offsets[0]), 0), p.M), left = blockIdx.y;
+            for (int g = 0; g < p.E && left >= 0; ++g) {
+                const int to = max(at, min(__ldg(&p.offsets[g + 1]), p.M));
+                if (to > at && left-- == 0) {
+                    found[0] = g;
+                    found[1] = at;
+                    found[2] = to - at;
+                }
+                at = to;
+            }
         }
         __syncthreads();
         if (found[1] < 0) return;

@@ -54,3 +54,68 @@ def test_weights_gradient_of_odd_widths_over_many_tiles(K, how):
         _check(outs[0][e], ref, mag, max(sizes[e], 1), odt)
     for other in outs[1:]:
         assert torch.equal(outs[0], other)
+
+
+def _few_rows(M, N, K, seed):
+    return _normal((M, K), torch.bfloat16, seed), torch.full((M + 64, N), 5.0, dtype=torch.bfloat16, device="cuda")
+
+
+@pytest.mark.parametrize("E", [256, 257, 512, 513, 1024])
+@pytest.mark.parametrize("M", [1, 10, 33, 59, 64])  # (64: 69 rows, the tensor-core kernel)
+def test_few_rows_of_many_groups(E, M):
+    """The few-row kernel's search for its group where a thread looks at several offsets: used groups anywhere in the
+    table, the first and the last among them, several rows in some, and unused rows before and behind."""
+    N, K = 40, 72
+    x, buf = _few_rows(M + 5, N, K, 31)
+    x[:2], x[2 + M:] = float("nan"), float("inf")
+    w = _normal((E, N, K), torch.bfloat16, 32, 0.05)
+    g = torch.Generator().manual_seed(M * E)
+    ids = torch.randint(0, E, (M,), generator=g)
+    ids[0] = E - 1
+    if M > 1:
+        ids[1] = 0
+    off = (torch.cat([torch.zeros(1).long(), torch.bincount(ids, minlength=E).cumsum(0)]) + 2).tolist()
+    out = buf[32:32 + M + 5]
+    moe.grouped_matmul(x, w, torch.tensor(off, dtype=torch.int32, device="cuda"), out=out)
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        if hi > lo:
+            a, b = x[lo:hi].double(), w[e].double().T
+            _check(out[lo:hi], a @ b, a.abs() @ b.abs(), K, torch.bfloat16)
+    assert bool((buf[:34] == 5).all()) and bool((buf[34 + M:] == 5).all())
+
+
+TABLES = [[0, -5, 4000, 20], [50, 20, 90, 10], [90, 90, 90, 90], [-9, -3, -1, 0], [0, 5, 2, 4], [7, 0, 0, 30, 12, 40],
+          [0, 40, 10, 40, 20, 40, 30, 40]]
+
+
+@pytest.mark.parametrize("table", TABLES, ids=str)
+@pytest.mark.parametrize("M", [3, 40, 64, 65, 300])
+@pytest.mark.parametrize("behind", [0, 600])
+def test_a_bad_table_is_made_ascending(table, M, behind):
+    """Whatever the table, and whichever kernel its size selects: offsets are clamped into [0, rows], an offset below an
+    earlier one counts as that one, and every row of the result is its group's product, or left as it was."""
+    N, K = 64, 72
+    x, buf = _few_rows(M, N, K, 33)
+    table = table + [table[-1]] * behind
+    E = len(table) - 1
+    w = _normal((E, N, K), torch.bfloat16, 34, 0.05)
+    off = torch.tensor(table, dtype=torch.int32, device="cuda")
+    out = buf[32:32 + M]
+    moe.grouped_matmul(x, w, off, out=out)
+    first = out.clone()
+    for _ in range(3):
+        assert torch.equal(first, moe.grouped_matmul(x, w, off, out=out))
+    o = torch.tensor(table).clamp(0, M).cummax(0).values.tolist()
+    seen = 0
+    for e in range(E):
+        a, b = x[o[e]:o[e + 1]].double(), w[e].double().T
+        if o[e + 1] > o[e]:
+            _check(out[o[e]:o[e + 1]], a @ b, a.abs() @ b.abs(), K, torch.bfloat16)
+            seen += o[e + 1] - o[e]
+    assert bool((buf[:32 + o[0]] == 5).all()) and bool((buf[32 + o[-1]:] == 5).all()) and seen == o[-1] - o[0]
+    dy = _normal((M, N), torch.bfloat16, 35)
+    dw = moe.grouped_matmul_wgrad(dy, x, off)
+    for e in range(min(E, 8)):
+        a, b = dy[o[e]:o[e + 1]].double().T, x[o[e]:o[e + 1]].double()
+        _check(dw[e], a @ b, a.abs() @ b.abs(), max(o[e + 1] - o[e], 1), torch.bfloat16)

@@ -67,8 +67,12 @@ constexpr int grouped_smem(bool small) { return grouped_stages(small) * grouped_
 // 16-wide step, an error that grows with the number of steps (measured: 3.5e-5
 // relative after 1875 steps), so the contraction is cut into parts of this
 // many K = 64 steps, each summed from zero and added in fp32 (round to nearest)
-// by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part.
+// by the epilogue: 6e-7.  16-bit results round at 2^-9 or 2^-12 and take one part
+// up to kLongPart steps (8192 values, whose rounding of equal signs stays under an
+// eighth of fp16's half step); longer contractions are summed in parts of that many
+// in one accumulator, and the epilogue adds them in fp32 in the other.
 constexpr int kPartSteps = 8;
+constexpr int kLongPart = 128;
 static_assert(grouped_smem(false) + 12 * (kGroupedMaxGroups + 16) <= 227 * 1024, "shared memory");
 
 struct GroupedMaps {
@@ -202,6 +206,19 @@ MOE_DEV int adapter_of(const AdapterArgs& p, int t) {
     const int id = __ldg(&p.ids[t]);
     return id >= 0 && id < p.L ? id : -1;
 }
+
+// The two accumulators' turns, the same for the MMA issuer and the epilogue: each
+// part of a contraction takes the other one, but a long tile of a 16-bit result
+// (stay) keeps one for all its parts, and the tile after it takes that one once
+// more: once it has been drained the epilogue is through with the other too,
+// where it holds the parts' sum.
+struct AccTurn {
+    uint32_t s = 0;  // bit 0: whose turn; 1, 2: parity of each one's uses; 3, 4: whether it has been used
+    MOE_DEV uint32_t b() const { return s & 1; }
+    MOE_DEV uint32_t parity() const { return (s >> (1 + b())) & 1; }
+    MOE_DEV bool used() const { return ((s >> (3 + b())) & 1) != 0; }
+    MOE_DEV void next(bool stay) { s = ((s ^ (2u << b())) | (8u << b())) ^ (stay ? 0u : 1u); }
+};
 
 template <int MODE, bool OUT32, bool ADAPT, bool SMALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
@@ -440,39 +457,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             const uint64_t bdesc = WG ? tc::sdesc_mn(b0, kPanel) : tc::sdesc(b0);
             constexpr uint32_t kA16 = (MODE == kGroupedForward ? 32 : 2048) >> 4, kB16 = (WG ? 2048 : 32) >> 4;
             bool ok = true;
-            int st = 0, it = 0;
+            int st = 0;
+            AccTurn turn;
             uint32_t phase = 0;
             for (int i = 0, t = pair; t < total && ok; t = tile_index(++i, pair, pairs)) {
                 const GroupedTile tl = tile_at<MODE>(g, t, list, JT);
                 const int KS = WG ? (tl.n + 63) >> 6 : KC + delta_steps(tl);
                 const uint32_t idesc = tc::idesc_f16_major(256, WG ? 256 : (tl.n + 31) & ~31, g.bf16 != 0,
                                                            MODE != kGroupedForward, WG);
+                const bool stay = !OUT32 && KS > kLongPart;
                 for (int s = 0; s < KS; ++s) {
-                    const int ps = OUT32 ? s % kPartSteps : s;
-                    if (ps == 0 && it > 1) {  // a new part: the next accumulator, once the epilogue has drained it
-                        ok = tc::bar_wait(&acce_bar[it & 1], ((it >> 1) - 1) & 1, g.status);
+                    constexpr int kPart = OUT32 ? kPartSteps : kLongPart;
+                    const int ps = s % kPart;
+                    if (ps == 0 && turn.used()) {  // a new part: the accumulator, once the epilogue has drained it
+                        ok = tc::bar_wait(&acce_bar[turn.b()], turn.parity() ^ 1, g.status);
                         if (!ok) break;
                     }
                     ok = tc::bar_wait(&full_bar[st], phase, g.status);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t acc = tmem + (it & 1) * 256;
+                    const uint32_t acc = tmem + turn.b() * 256;
                     const uint64_t ad = adesc + (uint32_t)(st * (kGroupedStage >> 4)), bd = bdesc + (uint32_t)(st * (kGroupedStage >> 4));
                     int kks = WG && s == KS - 1 ? (tl.n - s * 64 + 15) >> 4 : 4;
                     if constexpr (ADAPT) {
                         if (s >= KC) kks = (min(64, ex.args.r - (s - KC) % rank_blocks * 64) + 15) >> 4;
                     }
-                    const bool done = s == KS - 1 || (OUT32 && ps == kPartSteps - 1);
+                    const bool done = s == KS - 1 || ps == kPart - 1;
                     if (one) {
                         tc::mma_pair(acc, ad, bd, idesc, ps > 0 ? 1u : 0u);
 #pragma unroll
                         for (int kk = 1; kk < 4; ++kk)
                             if ((!WG && !ADAPT) || kk < kks) tc::mma_pair(acc, ad + kk * kA16, bd + kk * kB16, idesc, 1u);
                         tc::commit_pair(&empty_bar[st]);
-                        if (done) tc::commit_pair(&accf_bar[it & 1]);
+                        if (done) tc::commit_pair(&accf_bar[turn.b()]);
                     }
                     __syncwarp();
-                    if (done) ++it;
+                    if (done) turn.next(stay);
                     if (++st == kGroupedStages) {
                         st = 0;
                         phase ^= 1;
@@ -511,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
         uint8_t* stg = smem + kGroupedStages * kGroupedStage + (warp - 4) * (WG ? 2 : 1) * kEpiWarpBytes;
         const bool one = tc::elect_one();
         bool ok = true;
-        int it = 0;
+        AccTurn acc;
         uint32_t stores = 0;  // weights: tile stores issued; their number, not the column, says whose turn a buffer is
         const bool bf16 = g.bf16 != 0;
         if (ADAPT) grid_wait();  // v, from the kernel before
@@ -521,19 +541,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             if (empty && g.accumulate) continue;
             const int KS = WG ? (tl.n + 63) >> 6 : KC + delta_steps(tl);
             const bool by_hand = ADAPT && KS == KC && (!runs || one_adapter >= 0);  // deltas to add here
-            const int parts = OUT32 && !empty ? (KS + kPartSteps - 1) / kPartSteps : 1;
+            constexpr int kPart = OUT32 ? kPartSteps : kLongPart;
+            const int parts = empty ? 1 : (KS + kPart - 1) / kPart;
             for (int part = 0; part < parts; ++part) {
-                const int b = it & 1, use = it >> 1;
+                const uint32_t b = acc.b();
                 const bool add = OUT32 && (part > 0 || g.accumulate);
                 if (!empty) {
-                    ++it;
-                    if (lane == 0) ok = tc::bar_wait(&accf_bar[b], use & 1, g.status);
+                    if (lane == 0) ok = tc::bar_wait(&accf_bar[b], acc.parity(), g.status);
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     if (!ok) break;
+                    acc.next(!OUT32 && parts > 1);
                     tc::fence_after();
                 }
                 const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + b * 256;
                 const int f = tl.f0 + (int)rank * 128 + 32 * q;  // the warp's first feature
+                if (!OUT32 && parts > 1) {
+                    // A part of a long contraction: the sum so far is in the other accumulator's columns of this
+                    // warp, which it has read before (the MMAs leave them alone until this tile's last part is
+                    // drained).  The last part's sum goes back where the code below reads it
+                    const uint32_t other = tb ^ 256u, to = part == parts - 1 ? tb : other;
+                    const int most = WG ? min(256, g.C - tl.g0) : tl.n, step = WG ? 32 : 64;
+                    for (int c0 = WG ? 0 : 32 * turn; c0 < most; c0 += step)
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16], sum[16];
+                            tc::ld16_nowait(tb + c0 + h, v);
+                            if (part > 0) tc::ld16_nowait(other + c0 + h, sum);
+                            tc::ld_wait();
+                            if (part > 0)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(sum[i]));
+                            tc::st16(to + c0 + h, v);
+                        }
+                    tc::st_wait();
+                    if (part < parts - 1) {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::arrive_cluster_relaxed(tc::cluster_addr(&acce_bar[b], 0));
+                        continue;
+                    }
+                }
                 if (!WG) {
                     // 32 rows at a time.  TMEM is read as warp-MMA fragments, so an adapter's delta is added in
                     // registers; 16-bit results are packed in pairs and transposed by stmatrix into [row][32
@@ -552,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                     }
                     for (int c0 = 32 * turn; c0 < tl.n; c0 += 64) {
                         if constexpr (ADAPT) {
-                            if (by_hand && part == 0)
+                            if (by_hand && part == (OUT32 ? 0 : parts - 1))
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
                                     if (c0 + 16 * h < tl.n) {

@@ -70,6 +70,14 @@ MOE_DEV void ld16(uint32_t taddr, uint32_t (&r)[16]) {
     ld16_nowait(taddr, r);
     ld_wait();
 }
+MOE_DEV void st16(uint32_t taddr, const uint32_t (&r)[16]) {  // 16 columns of the warp's 32 lanes (no wait)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+MOE_DEV void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // four 8x8 16-bit matrices, transposed: lane l gives the address of row l % 8
 // of matrix l / 8; register j is that matrix's fragment

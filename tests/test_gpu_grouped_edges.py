@@ -119,3 +119,107 @@ def test_a_bad_table_is_made_ascending(table, M, behind):
     for e in range(min(E, 8)):
         a, b = dy[o[e]:o[e + 1]].double().T, x[o[e]:o[e + 1]].double()
         _check(dw[e], a @ b, a.abs() @ b.abs(), max(o[e + 1] - o[e], 1), torch.bfloat16)
+
+
+# Long contractions into 16 bits.  Up to 8192 values are summed by the tensor core, which rounds its accumulator towards
+# zero at each 16-wide step (at most two fp32 steps of it); longer ones in parts of 8192, added in fp32, half a step each.
+def _check_long(got, ref, mag, C, more=0.0):
+    f = torch.finfo(got.dtype)
+    steps = min(C, 8192) / 16 + 1 + C / 8192
+    bound = f.eps / 2 * ref.abs() + 2 * 2.0 ** -23 * steps * mag + more + f.tiny
+    off = got.double() - ref
+    assert not bool((off.abs() > bound).any()), f"worst {float((off.abs() / bound).max()):.3g} bounds, {int((off.abs() > bound).sum())} values"
+    return off
+
+
+def _positive(shape, dt, seed, lo, hi):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(shape, generator=g, device="cuda") * (hi - lo) + lo).to(dt)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("mode,C", [("weights", 300_008), ("weights", 8193), ("weights", 1_500_000), ("forward", 1 << 17),
+                                    ("forward", 8200), ("rows", 1 << 17), ("rows", 16392)])
+def test_long_sums_of_one_sign(mode, C, dtype):
+    """Nothing cancels, so rounding towards zero would add up: no value is further off than the parts allow."""
+    scale = 30000 / C / 0.75
+    if mode == "weights":
+        dy, x = _positive((C, 64), dtype, 41, 0.1, 0.2), _positive((C, 72), dtype, 42, scale * 3, scale * 7)
+        off = torch.tensor([0, C], dtype=torch.int32, device="cuda")
+        got = moe.grouped_matmul_wgrad(dy, x, off)[0]
+        ref = sum(p.double().T @ q.double() for p, q in zip(dy.split(1 << 18), x.split(1 << 18)))
+    else:
+        M, F = 300, 72
+        x, off = _positive((M, C), dtype, 43, 0.1, 0.2), torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        w = _positive((1, F, C) if mode == "forward" else (1, C, F), dtype, 44, scale * 3, scale * 7)
+        got = moe.grouped_matmul(x, w, off, transpose=mode == "rows")
+        ref = x.double() @ (w[0].double().T if mode == "forward" else w[0].double())
+    _check_long(got, ref, ref, C)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_long_sums_have_no_bias(dtype):
+    """Results spread over an octave and more, so that their roundings to 16 bits are of either sign: the mean of n of
+    them is within five standard deviations, half a step over sqrt(3 n), and the sums' own part as above.  (In the test
+    before, the results lie within 30 of 30000 and a bf16 step is 128: there all roundings share a sign.)"""
+    C = 300_008
+    dy = (_positive((C, 64), torch.float32, 54, 0.1, 0.2) * torch.linspace(1, 2, 64, device="cuda")).to(dtype)
+    x = (_positive((C, 72), torch.float32, 55, 0.1, 0.2) * torch.linspace(1, 1.4, 72, device="cuda")).to(dtype)
+    got = moe.grouped_matmul_wgrad(dy, x, torch.tensor([0, C], dtype=torch.int32, device="cuda"))[0]
+    ref = dy.double().T @ x.double()
+    off = _check_long(got, ref, ref, C)
+    noise = 5 * torch.finfo(dtype).eps / 2 / (3 * off.numel()) ** 0.5
+    assert float((off / ref).mean().abs()) <= 2 * 2.0 ** -23 * (8192 / 16 + 1 + C / 8192) + noise
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_long_and_short_tiles_follow_each_other(dtype):
+    """Groups above and below the length of a part, and empty ones, over several tiles a pair of SMs."""
+    sizes = [9000, 100, 0, 20000, 8192, 8193, 64, 8200, 1, 16385, 0, 500]
+    o = torch.tensor([0] + sizes).cumsum(0).tolist()
+    dy, x = _normal((o[-1], 1024), dtype, 45, 0.1), _normal((o[-1], 1096), dtype, 46, 0.1)
+    off = torch.tensor(o, dtype=torch.int32, device="cuda")
+    got = [moe.grouped_matmul_wgrad(dy, x, off) for _ in range(3)]
+    for e, n in enumerate(sizes):
+        a, b = dy[o[e]:o[e + 1]].double().T, x[o[e]:o[e + 1]].double()
+        _check_long(got[0][e], a @ b, a.abs() @ b.abs(), max(n, 1))
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("mode", ["forward", "rows"])
+def test_long_products_over_many_tiles(mode, dtype):
+    M, F, C = 2600, 2056, 16456  # three parts; 11 blocks by 9 tiles of features
+    x = _normal((M, C), dtype, 47)
+    w = _normal((3, F, C) if mode == "forward" else (3, C, F), dtype, 48, 0.02)
+    off = torch.tensor([3, 1500, 1600, M], dtype=torch.int32, device="cuda")
+    got = [moe.grouped_matmul(x, w, off, transpose=mode == "rows") for _ in range(2)]
+    for e, (lo, hi) in enumerate(((3, 1500), (1500, 1600), (1600, M))):
+        a, b = x[lo:hi].double(), w[e].double().T if mode == "forward" else w[e].double()
+        _check_long(got[0][lo:hi], a @ b, a.abs() @ b.abs(), C)
+        assert torch.equal(got[0][lo:hi], got[1][lo:hi])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("how", ["runs", "mixed"])
+@pytest.mark.parametrize("added", [False, True])
+def test_long_projection_with_adapters(how, added, dtype):
+    """A projection of a long contraction takes its deltas and its old values once, in the last part."""
+    T, N, K, r, L = 400, 264, 20008, 16, 3
+    x, w = _positive((T, K), dtype, 49, 0.1, 0.2), _positive((N, K), dtype, 50, 0.1, 0.2)
+    a, b = _normal((L, r, K), dtype, 51, K ** -0.5), _normal((L, N, r), dtype, 52, 5.0)
+    ids = torch.arange(T, device="cuda") // 150 if how == "runs" else torch.arange(T, device="cuda") % (L + 1)
+    before = _normal((T, N), dtype, 53, 100.0) if added else None
+    got = moe.adapter_project(x, a, b, ids.int(), w=w, out=before.clone() if added else None,
+                              flags=moe.MOE_ACCUMULATE if added else 0)
+    ref = x.double() @ w.double().T
+    mag, delta_mag = ref.clone(), torch.zeros_like(ref)
+    for i in range(L):
+        m = (ids == i).nonzero()[:, 0]
+        ref[m] += (x[m].double() @ a[i].double().T) @ b[i].double().T
+        delta_mag[m] = (x[m].double() @ a[i].double().abs().T) @ b[i].double().abs().T
+    if added:
+        ref, mag = ref + before.double(), mag + before.double().abs()
+    # v is held to 2^-16 (bf16, two terms) or 2^-22 of its value's terms, its sum takes K / 16 steps
+    v_terms = 2.0 ** -16 if dtype == torch.bfloat16 else 2.0 ** -22
+    _check_long(got, ref, mag, K, more=(2 * 2.0 ** -23 * (K / 16 + r + 16) + v_terms) * delta_mag)

@@ -29,7 +29,7 @@
 //               operands are cleared)
 //   warps 4-11  (weights: 4-7) epilogue: TMEM -> registers -> shared transpose -> 16-byte
 //               stores; two accumulators, so it overlaps the next tile's MMAs
-// Every wait is bounded.
+// Every wait is bounded, and covers at most kLongPart steps, or is given their number.
 //
 // What bounds it, and what it measures: a steady tile takes 530 cycles a K = 64
 // step where the tensor pipe alone needs 512, so large groups run at the tensor
@@ -513,7 +513,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             if (!(tl.n & 15)) continue;
             const int st = (j - 1) % kGroupedStages;
             ok = true;
-            if (lane == 0) ok = tc::bar_wait(&tail_bar[st], (phases >> st) & 1, g.status);
+            // (the whole contraction passes before its last step: one limit, 0.5 s, more for every 65536 steps, 18 ms)
+            if (lane == 0) ok = tc::bar_wait(&tail_bar[st], (phases >> st) & 1, g.status, 1 + (KS >> 16));
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
             phases ^= 1u << st;

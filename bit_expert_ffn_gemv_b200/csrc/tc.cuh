@@ -118,10 +118,12 @@ MOE_DEV bool test_wait(uint64_t* bar, uint32_t parity) {
 
 // bounded wait on an mbarrier phase; false if it gave up.  A non-blocking
 // test in a loop: the waiting thread sees the phase flip at once (a blocking
-// try_wait can leave it suspended for a while after the flip).
-MOE_DEV bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-    for (uint32_t it = 0; it < kSpin; ++it)
-        if (test_wait(bar, parity)) return true;
+// try_wait can leave it suspended for a while after the flip).  `limits`: for a
+// wait behind a known amount of work, how many times kSpin that may take.
+MOE_DEV bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t* status, int limits = 1) {
+    for (int l = 0; l < limits; ++l)
+        for (uint32_t it = 0; it < kSpin; ++it)
+            if (test_wait(bar, parity)) return true;
     flag_status(status, kStatusTimeout);
     return false;
 }

@@ -223,3 +223,28 @@ def test_long_projection_with_adapters(how, added, dtype):
     # v is held to 2^-16 (bf16, two terms) or 2^-22 of its value's terms, its sum takes K / 16 steps
     v_terms = 2.0 ** -16 if dtype == torch.bfloat16 else 2.0 ** -22
     _check_long(got, ref, mag, K, more=(2 * 2.0 ** -23 * (K / 16 + r + 16) + v_terms) * delta_mag)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_the_longest_group(out_dtype):
+    """As many rows as a call takes, in one group that ends inside a 16-row step: no wait runs out on the way (two
+    million steps take longer than a wait's basic limit), and the sums hold."""
+    M = (1 << 27) - 1
+    g = torch.Generator(device="cuda").manual_seed(61)
+    dy = torch.empty(M, 8, dtype=torch.bfloat16, device="cuda").uniform_(-1.0, 1.0, generator=g)
+    x = torch.empty(M, 8, dtype=torch.bfloat16, device="cuda").uniform_(-1.0, 1.0, generator=g)
+    x += dy  # (the diagonal grows with the rows)
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    got = moe.grouped_matmul_wgrad(dy, x, off, out_dtype=out_dtype)[0]
+    assert moe.moe_check_op_status() == 0
+    ref, mag = torch.zeros(8, 8, dtype=torch.float64, device="cuda"), torch.zeros(8, 8, dtype=torch.float64, device="cuda")
+    for p, q in zip(dy.split(1 << 22), x.split(1 << 22)):
+        ref += p.double().T @ q.double()
+        mag += p.double().abs().T @ q.double().abs()
+    part = 8192 if out_dtype == torch.bfloat16 else 512
+    # the parts' own steps, then one fp32 rounding of the sum so far for each part
+    bound = (torch.finfo(out_dtype).eps / 2 * ref.abs() + 2 * 2.0 ** -23 * (part / 16 + 1) * mag
+             + M / part * 2.0 ** -24 * ref.abs().clamp(min=float(mag.max()) * 2.0 ** -8))
+    off = (got.double() - ref).abs()
+    print("relative error", float((off / ref.abs().clamp(min=1e-9)).diag().max()))
+    assert not bool((off > bound).any()), f"worst {float((off / bound).max()):.3g} bounds"

@@ -307,6 +307,9 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
 PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
     HANDLE_TH_ERRORS
     arguments(count, 9);
+    const unsigned long flags = PyLong_AsUnsignedLong(a[7]);  // (the type is the tensors': MOE_OP_FP16 is none of them)
+    TORCH_CHECK_VALUE(!PyErr_Occurred() && !(flags & ~(unsigned long)(MOE_OUT_FP32 | MOE_ACCUMULATE)),
+                      "flags: a sum of MOE_OUT_FP32 and MOE_ACCUMULATE is expected");
     const Operand x = operand(a[0], "x");
     const Tensor &A = tensor(a[1], "a"), &B = tensor(a[2], "b");
     TORCH_CHECK_VALUE(A.dim() == 3 && B.dim() == 3, "a, b: contiguous [L, rank, k] and [L, n, rank] tensors are expected");
@@ -322,8 +325,6 @@ PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
         p.w = w.data_ptr();
     }
     p.scale = static_cast<const float*>(vector(a[5], "scale", x.dev, ScalarType::Float, L));
-    const unsigned long flags = PyLong_AsUnsignedLong(a[7]);
-    TORCH_CHECK_VALUE(!PyErr_Occurred() && flags <= UINT32_MAX, "flags: a sum of MOE_OUT_FP32 and MOE_ACCUMULATE is expected");
     TORCH_CHECK_VALUE(!(flags & MOE_ACCUMULATE) || a[6] != Py_None, "MOE_ACCUMULATE adds to a given out");
     const ScalarType type = (flags & MOE_OUT_FP32) ? ScalarType::Float : x.type;
     const Call call(a[8], x.dev);

@@ -63,5 +63,5 @@ def swiglu_backward(gu, dh, row_weights=None, dgu=None, h=None, drw=None, with_h
 def adapter_project(x, a, b, ids, w=None, scale=None, out=None, flags=0, stream=None):
     """[w x_t +] scale[i] * b[i] (a[i] x_t) for every token t with its adapter i = ids[t]: x [T, k], a [L, rank, k],
     b [L, n, rank], ids int32 [T], w [n, k], scale fp32 [L] -> [T, n], x's type, or fp32 with MOE_OUT_FP32 in flags.
-    With MOE_ACCUMULATE the result is added to out.  An id outside [0, L): no adapter."""
+    With MOE_ACCUMULATE the result is added to out; no other flag is taken (the type is x's).  An id outside [0, L): no adapter."""
     return _ops16.adapter_project(x, a, b, ids, w, scale, out, flags, stream)

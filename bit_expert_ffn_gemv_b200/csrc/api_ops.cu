@@ -99,7 +99,7 @@ moe_status moe_swiglu(const void* gu, int64_t ldgu, int32_t rows, int32_t f, con
     if (rows < 0 || rows > kMaxRows || !good_cols(f) || !good_ld(ldgu, 2 * (int64_t)f) || !good_ld(ldh, f))
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!good(gu) || !good(h) || !aligned4(row_weights) || !aligned4(n_rows)) return MOE_ERR_INVALID_ARG;
+    if (!good(gu) || !good(h) || !aligned4(row_weights) || !aligned4(n_rows) || h == gu) return MOE_ERR_INVALID_ARG;
     moe::SwigluArgs a{};
     a.gu = gu;
     a.ldgu = ldgu;
@@ -122,6 +122,10 @@ moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int
     if (rows == 0) return MOE_OK;
     if (!good(gu) || !good(dh) || !good(dgu) || (h && !aligned16(h)) || !aligned4(row_weights) || !aligned4(n_rows) ||
         !aligned4(d_row_weights))
+        return MOE_ERR_INVALID_ARG;
+    // in place only as the kernel can: every value of dgu by the lane that has read gu's at its address
+    if ((dgu == gu && lddgu != ldgu) || dgu == dh || (h && (h == gu || h == dh || h == dgu)) ||
+        (d_row_weights && d_row_weights == row_weights))
         return MOE_ERR_INVALID_ARG;
     moe::SwigluArgs a{};
     a.gu = gu;

@@ -56,7 +56,7 @@ def swiglu(gu, row_weights=None, out=None, n_rows=None, stream=None):
 
 def swiglu_backward(gu, dh, row_weights=None, dgu=None, h=None, drw=None, with_h=False, n_rows=None, stream=None):
     """Gradient of swiglu: (dgu [rows, 2f], h or None, d_row_weights or None).  h, the forward's result again, is
-    written when given or with_h; d_row_weights when row_weights is given."""
+    written when given or with_h; d_row_weights when row_weights is given.  dgu may be gu itself (in place)."""
     return _ops16.swiglu_backward(gu, dh, row_weights, dgu, h, drw, with_h, n_rows, stream)
 
 

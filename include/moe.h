@@ -412,7 +412,7 @@ const char* moe_kernel_name(int32_t kernel);
  *     ranges; rows before offsets[0] and from offsets[n_groups] on belong to
  *     no group: they are not read into any result, and their result rows are
  *     left as they were.  Values are clamped to [0, rows].
- *   - Results overlap no operand.
+ *   - Results overlap no operand, but moe_swiglu_backward's dgu may be gu itself.
  *   - rows = 0 is valid.  A device-side wait that ran out surfaces through
  *     moe_check_op_status.
  */
@@ -448,7 +448,7 @@ moe_status moe_grouped_wgrad(const void* dy, int64_t lddy, const void* x, int64_
  * product with an expert's gate rows followed by its up rows), h [rows x f].
  * row_weights (fp32 [rows]) may be NULL (1).  n_rows (device int32) may be NULL;
  * otherwise rows from *n_rows on are left as they were (pass offsets + n_groups).
- * Errors: INVALID_ARG, CUDA.
+ * Errors: INVALID_ARG (also h == gu), CUDA.
  */
 moe_status moe_swiglu(const void* gu, int64_t ldgu, int32_t rows, int32_t f, const float* row_weights,
                       const int32_t* n_rows, void* h, int64_t ldh, uint32_t flags, void* stream);
@@ -456,8 +456,9 @@ moe_status moe_swiglu(const void* gu, int64_t ldgu, int32_t rows, int32_t f, con
 /*
  * Gradient of moe_swiglu for dh [rows x f]: dgu [rows x 2f]; h [rows x f] (the
  * forward's result again, for the down matrices' gradient) and d_row_weights
- * (fp32 [rows], sum_j dh_j silu(g_j) u_j) are written unless NULL.
- * Errors: INVALID_ARG, CUDA.
+ * (fp32 [rows], sum_j dh_j silu(g_j) u_j) are written unless NULL.  dgu may be
+ * gu, with the same pitch.
+ * Errors: INVALID_ARG (also a result that is an operand or another result), CUDA.
  */
 moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int64_t lddh, int32_t rows, int32_t f,
                                const float* row_weights, const int32_t* n_rows, void* dgu, int64_t lddgu, void* h,

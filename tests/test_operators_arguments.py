@@ -15,3 +15,20 @@ def test_adapter_flags(flags, dtype):
     a, b = torch.zeros(1, 8, 64, dtype=dtype), torch.zeros(1, 32, 8, dtype=dtype)
     with pytest.raises(ValueError, match="flags"):
         moe.adapter_project(x, a, b, ids, flags=flags)
+
+
+P = 1 << 20  # a 16-byte aligned address (never read)
+GRAD = dict(gu=P, ldgu=128, dh=2 * P, lddh=64, rows=5, f=64, rw=6 * P, n_rows=0, dgu=3 * P, lddgu=128, h=4 * P, ldh=64, drw=5 * P, flags=0)
+
+
+@pytest.mark.parametrize("bad", [dict(dgu=P, lddgu=136), dict(dgu=2 * P), dict(h=P), dict(h=2 * P), dict(h=3 * P), dict(drw=6 * P)],
+                         ids=str)
+def test_swiglu_backward_over_an_operand(bad):
+    """A result may be no operand, but dgu gu itself, at gu's pitch."""
+    a = dict(GRAD, **bad)
+    assert moe.lib().moe_swiglu_backward(a["gu"], a["ldgu"], a["dh"], a["lddh"], a["rows"], a["f"], a["rw"], a["n_rows"], a["dgu"],
+                                         a["lddgu"], a["h"], a["ldh"], a["drw"], a["flags"], None) == 1
+
+
+def test_swiglu_over_its_operand():
+    assert moe.lib().moe_swiglu(P, 128, 5, 64, 0, 0, P, 128, 0, None) == 1

@@ -19,7 +19,17 @@
 
 namespace moe {
 
-MOE_DEV float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// s and 1 - s, from e^-|g|: the quotient's denominator lies in [1, 2], where the
+// fast division holds (it gives zero for denominators above 2^126, and with
+// e^-g those are the gates below -87.3, whose h a large u keeps from being
+// small), and neither value cancels.
+struct Sigmoid {
+    float s, rest;
+};
+MOE_DEV Sigmoid sigmoid(float g) {
+    const float z = __expf(-fabsf(g)), big = __fdividef(1.0f, 1.0f + z), small = z * big;
+    return g >= 0.0f ? Sigmoid{big, small} : Sigmoid{small, big};
+}
 
 constexpr int kSwigluThreads = 256;
 constexpr int kSwigluFewRows = 148 * 8 * 4;  // below this many rows a whole block takes each row
@@ -44,7 +54,7 @@ __global__ void __launch_bounds__(kSwigluThreads) swiglu_kernel(const SwigluArgs
         unpack8<BF16>(gv, g);
         unpack8<BF16>(uv, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = rw * (g[i] * sigmoid(g[i]) * u[i]);
+        for (int i = 0; i < 8; ++i) g[i] = rw * (g[i] * sigmoid(g[i]).s * u[i]);
         *reinterpret_cast<uint4*>(h + c) = pack8<BF16>(g);
     }
 }
@@ -88,10 +98,11 @@ __global__ void __launch_bounds__(kSwigluThreads, 4) swiglu_grad_kernel(const Sw
             unpack8<BF16>(dv[j], d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float s = sigmoid(g[i]), act = g[i] * s, act_u = act * u[i], dw = rw * d[i];
+                const Sigmoid sg = sigmoid(g[i]);
+                const float act = g[i] * sg.s, act_u = act * u[i], dw = rw * d[i];
                 hh[i] = rw * act_u;
                 dot = fmaf(d[i], act_u, dot);
-                g[i] = dw * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+                g[i] = dw * (sg.s * (1.0f + g[i] * sg.rest)) * u[i];  // (dh u may overflow where the product does not)
                 u[i] = dw * act;
             }
             *reinterpret_cast<uint4*>(dgu + c) = pack8<BF16>(g);

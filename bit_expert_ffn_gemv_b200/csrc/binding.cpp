@@ -13,6 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -40,7 +41,10 @@ PyObject* raise_status(moe_status s, const char* what) {
 
 const Tensor& tensor(PyObject* o, const char* name) {
     TORCH_CHECK_TYPE(THPVariable_Check(o), name, ": a tensor is expected");
-    return THPVariable_Unpack(o);
+    const Tensor& t = THPVariable_Unpack(o);
+    TORCH_CHECK_VALUE(!(t.requires_grad() && at::GradMode::is_enabled()), name,
+                      ": requires a gradient, and this call records none (detach it, or call under torch.no_grad())");
+    return t;
 }
 
 struct Operand {  // the matrix that sets a call's type and device
@@ -106,6 +110,8 @@ struct Result {
     PyObject* given = nullptr;
     PyObject* object() {
         if (given) {
+            // written behind autograd's back: a graph that saved it has to see that
+            if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
             Py_INCREF(given);
             return given;
         }

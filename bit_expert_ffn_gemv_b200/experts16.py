@@ -5,7 +5,8 @@ moe_adapter_project in include/moe.h).  The checks of types, shapes and strides,
 are in csrc/binding.cpp (module _ops16): ValueError for tensors that do not fit, MoeError for what the library
 refuses.  Work is enqueued on ``stream`` (a torch.cuda.Stream; default: the current stream of the tensors' device),
 and a result that is not given is allocated for that stream.  No call synchronises.  There is no autograd: the
-gradients are calls of their own.
+gradients are calls of their own, and while gradients are recorded a tensor that requires one is refused (detach it,
+or call under torch.no_grad()).
 
 Rows are (token, expert) pairs sorted by expert; ``offsets`` (int32 [E + 1], on the device) gives each expert's row
 range.  An expert FFN and its gradient, for gate/up matrices w1 [E, 2f, d] and down matrices w2 [E, d, f]:

@@ -32,3 +32,25 @@ def test_swiglu_backward_over_an_operand(bad):
 
 def test_swiglu_over_its_operand():
     assert moe.lib().moe_swiglu(P, 128, 5, 64, 0, 0, P, 128, 0, None) == 1
+
+
+CALLS = {  # each operator with one tensor argument after the other requiring a gradient
+    "grouped_matmul": lambda t: moe.grouped_matmul(t["x"], t["w"], t["ids"], out=t["out"]),
+    "grouped_matmul_wgrad": lambda t: moe.grouped_matmul_wgrad(t["x"], t["w"], t["ids"], out=t["out"]),
+    "swiglu": lambda t: moe.swiglu(t["x"], t["rw"], out=t["out"]),
+    "swiglu_backward": lambda t: moe.swiglu_backward(t["x"], t["w"], t["rw"], dgu=t["out"]),
+    "adapter_project": lambda t: moe.adapter_project(t["x"], t["w"], t["b"], t["ids"], scale=t["rw"], out=t["out"]),
+}
+
+
+@pytest.mark.parametrize("op", CALLS)
+def test_a_tensor_that_requires_a_gradient(op):
+    """No call records a gradient, so none takes a tensor that needs one while gradients are recorded."""
+    t = {"x": torch.zeros(4, 64, dtype=torch.bfloat16), "w": torch.zeros(1, 8, 64, dtype=torch.bfloat16),
+         "b": torch.zeros(1, 32, 8, dtype=torch.bfloat16), "ids": torch.zeros(4, dtype=torch.int32),
+         "out": torch.zeros(4, 32, dtype=torch.bfloat16), "rw": torch.zeros(4)}
+    t["x"].requires_grad_(True)
+    with pytest.raises(ValueError, match="gradient"):
+        CALLS[op](t)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        CALLS[op](t)

@@ -144,6 +144,8 @@ def lib() -> ctypes.CDLL:
             L.moe_adapter_workspace.argtypes = [i32, i32]
             L.moe_adapter_project.restype = st
             L.moe_adapter_project.argtypes = [ctypes.POINTER(MoeAdapterArgs), u32, vp]
+            L.moe_adapter_check.restype = st
+            L.moe_adapter_check.argtypes = [ctypes.POINTER(MoeAdapterArgs), u32]
             L.moe_check_op_status.restype = st
             L.moe_check_op_status.argtypes = []
             L.moe_status_string.restype = ctypes.c_char_p
@@ -331,11 +333,15 @@ class MoeLayer:
         term is added to the layer's result: a bf16 y is rounded by the layer and again by the sum, an fp32 y
         (MOE_OUT_FP32) not at all.  y == x (a residual update in place) needs MOE_NORM_INPUT, whose normalised copy
         the adapters read.  With a handle restricted to an expert range, add the adapters on one rank only.
+        Tensors that do not fit are refused before y is written: x and y are contiguous [T, d], x bf16.
         """
         import torch
-        from .experts16 import adapter_project
+        from .experts16 import _ops16, adapter_project
         if y is not None and y.data_ptr() == x.data_ptr() and not flags & MOE_NORM_INPUT:
             raise ValueError("y == x: the adapters read x after the layer has updated it (use MOE_NORM_INPUT)")
+        if y is None and flags & MOE_ACCUMULATE:
+            raise ValueError("MOE_ACCUMULATE adds to a given y")
+        _ops16.adapter_beside(x, a, b, ids, scale, y, flags & MOE_OUT_FP32, self.cfg.d, stream)
         # (on the stream: what is allocated here is freed, or handed out, before the calls have run)
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
             u = rms_normalize(x, stream=stream) if flags & MOE_NORM_INPUT else x

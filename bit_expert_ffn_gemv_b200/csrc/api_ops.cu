@@ -149,7 +149,7 @@ size_t moe_adapter_workspace(int32_t tokens, int32_t rank) {
     return moe::adapter_workspace(tokens, rank);
 }
 
-moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, void* stream) {
+moe_status moe_adapter_check(const moe_adapter_args* args, uint32_t flags) {
     if (!args || (flags & ~(MOE_OUT_FP32 | MOE_ACCUMULATE | MOE_OP_FP16))) return MOE_ERR_INVALID_ARG;
     const moe_adapter_args& q = *args;
     if (q.tokens < 0 || q.tokens > kMaxRows || !good_cols(q.n) || !good_cols(q.k) || q.n_adapters < 1 ||
@@ -160,6 +160,13 @@ moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, voi
         !q.ids || !aligned4(q.ids) || !aligned4(q.scale) ||
         q.workspace_bytes < moe_adapter_workspace(q.tokens, q.rank) || q.x == q.y)
         return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, void* stream) {
+    const moe_status st = moe_adapter_check(args, flags);
+    if (st != MOE_OK || args->tokens == 0) return st;
+    const moe_adapter_args& q = *args;
     moe::AdapterArgs a{};
     a.x = q.x;
     a.ldx = q.ldx;

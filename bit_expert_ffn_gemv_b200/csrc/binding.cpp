@@ -309,33 +309,36 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     END_HANDLE_TH_ERRORS
 }
 
-// x, a, b, ids, w, scale, out, flags, stream
-PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
-    HANDLE_TH_ERRORS
-    arguments(count, 9);
-    const unsigned long flags = PyLong_AsUnsignedLong(a[7]);  // (the type is the tensors': MOE_OP_FP16 is none of them)
+// The arguments of an adapter call but its result and workspace, checked.
+struct Adapter {
+    const Operand x;
+    moe_adapter_args p{};
+    uint32_t flags;
+    ScalarType type;  // of the result
+};
+uint32_t adapter_flags(PyObject* o) {
+    const unsigned long flags = PyLong_AsUnsignedLong(o);  // (the type is the tensors': MOE_OP_FP16 is none of them)
     TORCH_CHECK_VALUE(!PyErr_Occurred() && !(flags & ~(unsigned long)(MOE_OUT_FP32 | MOE_ACCUMULATE)),
                       "flags: a sum of MOE_OUT_FP32 and MOE_ACCUMULATE is expected");
-    const Operand x = operand(a[0], "x");
-    const Tensor &A = tensor(a[1], "a"), &B = tensor(a[2], "b");
+    return (uint32_t)flags;
+}
+Adapter adapter(PyObject* ox, PyObject* oa, PyObject* ob, PyObject* oids, PyObject* ow, PyObject* oscale, uint32_t flags) {
+    Adapter r{operand(ox, "x"), {}, 0, ScalarType::Float};
+    const Operand& x = r.x;
+    const Tensor &A = tensor(oa, "a"), &B = tensor(ob, "b");
     TORCH_CHECK_VALUE(A.dim() == 3 && B.dim() == 3, "a, b: contiguous [L, rank, k] and [L, n, rank] tensors are expected");
     const int64_t L = A.size(0), rank = A.size(1), n = B.size(1), k = x.cols;
     block(A, "a", x.dev, x.type, {L, rank, k});
     block(B, "b", x.dev, x.type, {L, n, rank});
-    TORCH_CHECK_VALUE(a[3] != Py_None, "ids: a tensor is expected");
-    moe_adapter_args p{};
-    p.ids = static_cast<const int32_t*>(vector(a[3], "ids", x.dev, ScalarType::Int, x.rows));
-    if (a[4] != Py_None) {
-        const Tensor& w = tensor(a[4], "w");
+    TORCH_CHECK_VALUE(oids != Py_None, "ids: a tensor is expected");
+    moe_adapter_args& p = r.p;
+    p.ids = static_cast<const int32_t*>(vector(oids, "ids", x.dev, ScalarType::Int, x.rows));
+    if (ow != Py_None) {
+        const Tensor& w = tensor(ow, "w");
         block(w, "w", x.dev, x.type, {n, k});
         p.w = w.data_ptr();
     }
-    p.scale = static_cast<const float*>(vector(a[5], "scale", x.dev, ScalarType::Float, L));
-    TORCH_CHECK_VALUE(!(flags & MOE_ACCUMULATE) || a[6] != Py_None, "MOE_ACCUMULATE adds to a given out");
-    const ScalarType type = (flags & MOE_OUT_FP32) ? ScalarType::Float : x.type;
-    const Call call(a[8], x.dev);
-    Result y = result(a[6], "out", {x.rows, n}, x.t, type);
-    p.ldy = matrix(of(y), "out", x.dev, type, x.rows, n);
+    p.scale = static_cast<const float*>(vector(oscale, "scale", x.dev, ScalarType::Float, L));
     p.x = x.t.data_ptr();
     p.ldx = x.ld;
     p.tokens = int32(x.rows, "tokens");
@@ -345,13 +348,55 @@ PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
     p.b = B.data_ptr();
     p.n_adapters = int32(L, "L");
     p.rank = int32(rank, "rank");
-    p.y = of(y).data_ptr();
     p.workspace_bytes = moe_adapter_workspace(p.tokens, p.rank);
-    const Tensor workspace = at::empty({(int64_t)p.workspace_bytes}, x.t.options().dtype(ScalarType::Byte));
+    r.flags = flags | type_flag(x.type);
+    r.type = (flags & MOE_OUT_FP32) ? ScalarType::Float : x.type;
+    return r;
+}
+
+// x, a, b, ids, w, scale, out, flags, stream
+PyObject* adapter_project(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    arguments(count, 9);
+    const uint32_t flags = adapter_flags(a[7]);
+    Adapter c = adapter(a[0], a[1], a[2], a[3], a[4], a[5], flags);
+    moe_adapter_args& p = c.p;
+    TORCH_CHECK_VALUE(!(flags & MOE_ACCUMULATE) || a[6] != Py_None, "MOE_ACCUMULATE adds to a given out");
+    const Call call(a[8], c.x.dev);
+    Result y = result(a[6], "out", {c.x.rows, p.n}, c.x.t, c.type);
+    p.ldy = matrix(of(y), "out", c.x.dev, c.type, c.x.rows, p.n);
+    p.y = of(y).data_ptr();
+    const Tensor workspace = at::empty({(int64_t)p.workspace_bytes}, c.x.t.options().dtype(ScalarType::Byte));
     p.workspace = workspace.data_ptr();
-    const moe_status s = moe_adapter_project(&p, (uint32_t)flags | type_flag(x.type), call.stream);
+    const moe_status s = moe_adapter_project(&p, c.flags, call.stream);
     if (s != MOE_OK) return raise_status(s, "moe_adapter_project");
     return y.object();
+    END_HANDLE_TH_ERRORS
+}
+
+// What MoeLayer.forward_adapted needs before the layer writes y: x [T, d] bf16 and y (or None) [T, d] contiguous, and
+// adapters of this shape that the operator takes.
+// x, a, b, ids, scale, y, flags, d, stream
+PyObject* adapter_beside(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    arguments(count, 9);
+    Adapter c = adapter(a[0], a[1], a[2], a[3], Py_None, a[4], adapter_flags(a[6]));
+    moe_adapter_args& p = c.p;
+    const int64_t d = PyLong_AsLongLong(a[7]);
+    TORCH_CHECK_VALUE(c.x.type == ScalarType::BFloat16 && c.x.cols == d && c.x.t.is_contiguous(),
+                      "x: a contiguous [T, ", d, "] bf16 tensor is expected, not ", c.x.t.sizes(), " of ", c.x.t.scalar_type());
+    TORCH_CHECK_VALUE(p.n == d, "b: ", d, " features are expected, not ", p.n);
+    p.ldy = d;
+    p.y = p.workspace = reinterpret_cast<void*>(16);  // (to be allocated: aligned)
+    if (a[5] != Py_None) {
+        const Tensor& y = tensor(a[5], "y");
+        block(y, "y", c.x.dev, c.type, {c.x.rows, d});
+        if (y.data_ptr() != p.x) p.y = y.data_ptr();  // (y may be x, where the adapters read the normalised copy)
+    }
+    const Call call(a[8], c.x.dev);  // (a stream of another device)
+    const moe_status s = moe_adapter_check(&p, c.flags);
+    if (s != MOE_OK) return raise_status(s, "moe_adapter_check");
+    Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
 
@@ -367,6 +412,7 @@ PyMethodDef kMethods[] = {{"grouped_matmul", FAST(grouped_matmul), nullptr},
                           {"swiglu", FAST(swiglu), nullptr},
                           {"swiglu_backward", FAST(swiglu_backward), nullptr},
                           {"adapter_project", FAST(adapter_project), nullptr},
+                          {"adapter_beside", FAST(adapter_beside), nullptr},
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ops16", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -504,6 +504,13 @@ size_t moe_adapter_workspace(int32_t tokens, int32_t rank);
 moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, void* stream);
 
 /*
+ * moe_adapter_project's checks alone: MOE_OK or INVALID_ARG, nothing is enqueued.
+ * For a caller that has a layer write y first and would have it left as it was
+ * where the adapters are refused.
+ */
+moe_status moe_adapter_check(const moe_adapter_args* args, uint32_t flags);
+
+/*
  * Synchronise the current device and return the first device-side error that
  * one of these operators recorded on it since the last call (then clear it):
  * MOE_ERR_TIMEOUT or MOE_OK; MOE_ERR_CUDA if the synchronisation failed.

@@ -54,3 +54,15 @@ def test_a_tensor_that_requires_a_gradient(op):
         CALLS[op](t)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         CALLS[op](t)
+
+
+def test_adapter_check():
+    """moe_adapter_check is moe_adapter_project's refusals, without the call."""
+    import ctypes
+    good = dict(x=P, ldx=64, tokens=10, n=32, k=64, w=0, a=P, b=P, scale=0, ids=P, n_adapters=3, rank=16, y=2 * P, ldy=32,
+                workspace=P, workspace_bytes=1 << 20)
+    check = moe.lib().moe_adapter_check
+    assert check(ctypes.byref(moe.MoeAdapterArgs(**good)), 0x3) == 0
+    assert check(None, 0) == 1 and check(ctypes.byref(moe.MoeAdapterArgs(**good)), 0x4) == 1
+    for bad in (dict(rank=12), dict(y=P), dict(a=P + 8), dict(ids=0), dict(n=4), dict(ldy=24), dict(workspace_bytes=8)):
+        assert check(ctypes.byref(moe.MoeAdapterArgs(**dict(good, **bad))), 0) == 1

@@ -2,12 +2,16 @@
 // their delta B_a v_t in warp-MMA fragments.
 //
 // v is fp32; the MMA takes 16-bit operands, so v is split into terms of B's
-// type (v = hi + lo [+ lower], each exact in what the ones before leave): two
-// terms hold 16 bits of v in bf16 and 22 in fp16, three hold 24 in bf16, which
-// fp32 results use.  The split is made once, where v is computed.  fp16's range
-// is too small for v: a token whose largest value lies outside [2^-2, 2^15) is
-// first scaled by a power of two that brings it into [1, 2), undone in the
-// result (inside the range the two terms hold 2^-23 of that largest value).
+// type (v = hi + lo [+ lower], each exact in what the ones before leave): three
+// bf16 terms hold all 24 bits of v, two fp16 terms 22.  Fewer would show: where
+// W x, the old y or the other rank values cancel a delta, what v leaves out is
+// the result.  (Two bf16 terms leave out 2^-17 of v, and 8192 tokens of eight
+// requests beside 2048 x 2048 at rank 32 take 71.3 us with them, 73.4 with three;
+// the delta alone at rank 16 36.7 and 43.9.)  The split is made once, where v is
+// computed.  fp16's range is too small for v: a token whose largest value lies
+// outside [2^-2, 2^15) is first scaled by a power of two that brings it into
+// [1, 2), undone in the result.  Either way the two terms hold each value to
+// 2^-23 of the token's largest.
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
@@ -15,13 +19,15 @@
 
 namespace moe {
 
+constexpr int adapter_terms(bool bf16) { return bf16 ? 3 : 2; }
+
 // Split v: `terms` row-major 16-bit matrices [T x r], then (fp16) the factor
 // that undoes each token's scale.  fp32 v: [T x r].
 MOE_DEV const uint16_t* adapter_term(const AdapterArgs& p, int term) {
     return static_cast<const uint16_t*>(p.v) + (int64_t)term * p.T * p.r;
 }
-MOE_DEV float* adapter_back(const AdapterArgs& p, int terms) {
-    return reinterpret_cast<float*>(static_cast<uint16_t*>(p.v) + (int64_t)terms * p.T * p.r);
+MOE_DEV float* adapter_back(const AdapterArgs& p) {  // (fp16)
+    return reinterpret_cast<float*>(static_cast<uint16_t*>(p.v) + (int64_t)adapter_terms(false) * p.T * p.r);
 }
 
 // the next term of a value, and what it leaves (an infinite term leaves nothing)
@@ -44,8 +50,9 @@ MOE_DEV uint16_t take_term(float& v) {
 // after these (next .. next + n_next - 1) are fetched into L1.  Lane l / 4 reads
 // token l / 4 (+ 8) and feature rows l / 4 + 8 i; lane l % 4 takes eight
 // consecutive rank values of each, the same for both operands.
-template <bool BF16, int TERMS>
+template <bool BF16>
 MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next, int f0, uint32_t* lo, uint32_t* hi) {
+    constexpr int TERMS = adapter_terms(BF16);
     const int lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
     int id = lane < n ? __ldg(&p.ids[t0 + lane]) : -1;
     int id_next = lane < n_next ? __ldg(&p.ids[next + lane]) : -1;
@@ -64,7 +71,7 @@ MOE_DEV void add_delta(const AdapterArgs& p, int t0, int n, int next, int n_next
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = 8 * (i >> 1) + 2 * c + (i & 1);
-        back[i] = !BF16 && ((all >> t) & 1) ? adapter_back(p, TERMS)[t0 + t] : 1.f;
+        back[i] = !BF16 && ((all >> t) & 1) ? adapter_back(p)[t0 + t] : 1.f;
     }
     int64_t at[4];  // offset of feature rows f0 + gq + 8 i in one adapter's B (past N: any row, not stored)
 #pragma unroll

@@ -6,11 +6,14 @@
 // Two launches.  The first computes v for every token; the second starts
 // while the first still runs (programmatic dependent launch), streams W, and
 // waits for v only before it adds the delta:
-//   shrink_kernel   v, from windows of 32 tokens by slices of K
+//   shrink_kernel   v, from windows of 8 or 32 tokens by slices of K
 //   skinny_kernel   up to 64 tokens: W by warp MMAs, straight from HBM
-//   grouped_kernel  more tokens: W on the tensor cores (grouped.cu), the delta in its epilogue
+//   grouped_kernel  more tokens: W on the tensor cores (grouped.cu), and with it the delta of runs
+//                   of one adapter, as further steps; of mixed tokens it is added in the epilogue
 //   expand_kernel   no W: the delta alone
-// v and the delta stay in fp32, so the result is rounded once.
+// v is summed in fp32.  Up to 64 tokens with W the delta is fp32 arithmetic too;
+// the other forms multiply v as 16-bit terms that hold all of it (bf16), or 2^-23
+// of a token's largest value (fp16; adapter.cuh).  The result is rounded once.
 #include <cuda_runtime.h>
 
 #include "adapter.cuh"
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                 scale = __uint_as_float((uint32_t)(254 - e) << 23);
                 back = __uint_as_float((uint32_t)e << 23);
             }
-            if (lane == 0) adapter_back(p, TERMS)[t0 + m] = back;
+            if (lane == 0) adapter_back(p)[t0 + m] = back;
         }
         uint16_t* out = static_cast<uint16_t*>(p.v) + row + lane;
 #pragma unroll
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
 // wait for v.
 template <bool BF16, bool OUT32>
 __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
-    constexpr int TERMS = BF16 && OUT32 ? 3 : 2, PAIRS = 4;  // pairs of column tiles: 16 features each
+    constexpr int TERMS = adapter_terms(BF16), PAIRS = 4;  // pairs of column tiles: 16 features each
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
     const int f0 = (blockIdx.y * 4 + warp) * 16 * PAIRS, t0 = blockIdx.x * 16, n = min(16, p.T - t0);
     if (f0 >= p.N) return;
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (!use[h]) continue;  // (another adapter's infinities must not reach this token)
-            const float back = BF16 ? 1.f : adapter_back(p, TERMS)[t0 + gq + 8 * h];
+            const float back = BF16 ? 1.f : adapter_back(p)[t0 + gq + 8 * h];
 #pragma unroll
             for (int t = 0; t < PAIRS; ++t)
 #pragma unroll
@@ -422,7 +425,7 @@ static cudaError_t shrink(const AdapterArgs& p, cudaStream_t s) {
 
 template <bool BF16, bool OUT32>
 static cudaError_t adapters(AdapterArgs p, cudaStream_t s) {
-    constexpr int kTerms = BF16 && OUT32 ? 3 : 2;
+    constexpr int kTerms = adapter_terms(BF16);
     p.slices = shrink_slices(p.T, p.K);
     const bool skinny = p.w && p.T <= kSkinnyMaxRows;
     const cudaError_t e = skinny                        ? shrink<BF16, 8, 0>(p, s)

@@ -196,8 +196,8 @@ struct GroupedExtra<true> {
 };
 
 // Tokens [row0, row0 + n) whose v's terms are unscaled (fp16; adapter.cuh); a warp.
-MOE_DEV bool unscaled(const AdapterArgs& p, int terms, int row0, int n) {
-    const float* back = adapter_back(p, terms) + row0;
+MOE_DEV bool unscaled(const AdapterArgs& p, int row0, int n) {
+    const float* back = adapter_back(p) + row0;
     bool ok = true;
     for (int i = threadIdx.x & 31; i < n; i += 32) ok = ok && back[i] == 1.f;
     return __all_sync(0xffffffffu, ok);
@@ -356,11 +356,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
     // Adapters: steps that add a tile's delta, v's terms times B in 64-wide
     // blocks of the rank; 0 where there is none or the epilogue adds it.  Whole
     // warps.  (fp16: v must be there to see whether it was scaled.)
-    constexpr int kTerms = OUT32 ? 3 : 2;  // fp16: always 2
     int rank_blocks = 0, terms = 0, one_adapter = -1;
     if constexpr (ADAPT) {
         rank_blocks = (ex.args.r + 63) >> 6;
-        terms = g.bf16 ? kTerms : 2;
+        terms = adapter_terms(g.bf16 != 0);
     }
     auto delta_steps = [&](const GroupedTile& tl) -> int {
         if constexpr (ADAPT) {
@@ -368,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
             if (one_adapter < 0) return 0;
             if (!g.bf16) {
                 grid_wait();
-                if (!unscaled(ex.args, terms, tl.row0, tl.n)) return 0;
+                if (!unscaled(ex.args, tl.row0, tl.n)) return 0;
             }
             return terms * rank_blocks;
         }
@@ -607,8 +606,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupedThreads, 1)
                                         const int t0 = tl.row0 + c0 + 16 * h, left = tl.n - c0 - 16 * h;
                                         const int skip = h ? 48 : 16;  // to the warp's next 16 rows
                                         const int m = min(16, left), mn = min(16, left - skip);
-                                        if (bf16) add_delta<true, kTerms>(ex.args, t0, m, t0 + skip, mn, f, &r[0][8 * h], &r[1][8 * h]);
-                                        else add_delta<false, 2>(ex.args, t0, m, t0 + skip, mn, f, &r[0][8 * h], &r[1][8 * h]);
+                                        if (bf16) add_delta<true>(ex.args, t0, m, t0 + skip, mn, f, &r[0][8 * h], &r[1][8 * h]);
+                                        else add_delta<false>(ex.args, t0, m, t0 + skip, mn, f, &r[0][8 * h], &r[1][8 * h]);
                                     }
                         }
                         if (ADAPT && !OUT32 && g.accumulate) {  // y's values, added before the one rounding
@@ -833,7 +832,7 @@ static cudaError_t adapter_launch(const AdapterArgs& p, bool bf16, cudaStream_t 
     {
         const cuuint64_t bd[3] = {(cuuint64_t)p.r, (cuuint64_t)p.N, (cuuint64_t)p.L};
         const cuuint64_t bs[2] = {(cuuint64_t)p.r * 2, (cuuint64_t)p.N * p.r * 2};
-        const cuuint64_t vd[3] = {(cuuint64_t)p.r, (cuuint64_t)p.T, bf16 && OUT32 ? 3u : 2u};
+        const cuuint64_t vd[3] = {(cuuint64_t)p.r, (cuuint64_t)p.T, (cuuint64_t)adapter_terms(bf16)};
         const cuuint64_t vs[2] = {(cuuint64_t)p.r * 2, (cuuint64_t)p.T * p.r * 2};
         const cuuint32_t big[3] = {64, 128, 1}, small[3] = {64, 32, 1};
         e = encode_tiles(&ex.b, elem16(bf16), p.b, 3, bd, bs, big, 128);

@@ -472,8 +472,10 @@ moe_status moe_swiglu_backward(const void* gu, int64_t ldgu, const void* dh, int
  * MOE_ACCUMULATE.  A token whose id lies outside [0, n_adapters) has no adapter
  * term (without w and MOE_ACCUMULATE its row is zeros).  Tokens may come in any
  * order of ids; runs of one adapter are fastest.  Adapters of a smaller rank
- * are padded with zeros.  The inner product A x and the sum stay in fp32; y is
- * rounded once.
+ * are padded with zeros.  The inner product A x and the sum are fp32 (with fp16
+ * operands and more than 64 tokens, or no W, A x enters the second product to
+ * 2^-23 of the token's largest value); y is rounded once.  Infinities in B give
+ * infinities or NaN in their token's row.
  */
 typedef struct {
     const void* x;      /* [tokens x k], pitch ldx */

@@ -35,7 +35,16 @@ struct SkinnyArgs {
     AdapterArgs ad;      // adapter form
 };
 
-template <bool BF16, int NB>
+// A warp MMA rounds its accumulator towards zero at each step, like the tensor
+// core's tiles (grouped.cu), so a warp's sum is cut into parts of this many values,
+// added in fp32 in the place in shared memory where the warps' sums meet.  A warp's
+// share of K is an eighth, so up to K = 4096 there is one part, and a kernel that
+// looks for none (LONG false; K = 2048: 64 rows of one matrix 6.9 us, 7.25 looking;
+// one token's product 13.8 and 14.0).  K = 2^17, values of one sign: 7.6e-5 off in
+// one part, 3e-7 in parts.
+constexpr int kSkinnyPart = 512;
+
+template <bool BF16, int NB, bool LONG>
 MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t* x, int64_t ldx, int n, int kb, int ke,
                          float* red, int pitch) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, c = lane & 3;
@@ -55,8 +64,22 @@ MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t*
             mma16<BF16>(acc[b], f1, bv[b].z, bv[b].w);
         }
     };
-    int k0 = kb;
+    auto each = [&](auto use) {  // this lane's sums, [feature][row]
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            use(red[gq * pitch + b * 8 + 2 * c], acc[b][0]);
+            use(red[gq * pitch + b * 8 + 2 * c + 1], acc[b][1]);
+            use(red[(gq + 8) * pitch + b * 8 + 2 * c], acc[b][2]);
+            use(red[(gq + 8) * pitch + b * 8 + 2 * c + 1], acc[b][3]);
+        }
+    };
+    int k0 = kb, part = kb;  // part: where the part in acc began
     for (; k0 + 32 * U <= ke; k0 += 32 * U) {
+        if (LONG && k0 - part == kSkinnyPart) {
+            if (part == kb) each([](float& sum, float& a) { sum = a; a = 0.f; });
+            else each([](float& sum, float& a) { sum += a; a = 0.f; });
+            part = k0;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             lo[u] = __ldcs(reinterpret_cast<const uint4*>(w0 + k0 + 32 * u));
@@ -86,20 +109,14 @@ MOE_DEV void skinny_sums(const uint16_t* w0, const uint16_t* w1, const uint16_t*
             multiply(u, bv);
         }
     }
-    // [feature][row]
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        red[gq * pitch + b * 8 + 2 * c] = acc[b][0];
-        red[gq * pitch + b * 8 + 2 * c + 1] = acc[b][1];
-        red[(gq + 8) * pitch + b * 8 + 2 * c] = acc[b][2];
-        red[(gq + 8) * pitch + b * 8 + 2 * c + 1] = acc[b][3];
-    }
+    if (LONG && part != kb) each([](float& sum, float& a) { sum += a; });
+    else each([](float& sum, float& a) { sum = a; });
 }
 
 // MAXNB: blocks of 8 rows that a group can have (the call's rows, rounded up).
 // PER_SM: CTAs an SM must hold; one, where there is no second, leaves registers
 // for all of x's loads in flight.
-template <bool BF16, bool OUT32, bool ADAPT, int MAXNB, int PER_SM = 2>
+template <bool BF16, bool OUT32, bool ADAPT, bool LONG, int MAXNB, int PER_SM = 2>
 __global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const SkinnyArgs p) {
     constexpr int kPitch = 8 * MAXNB + 1;
     __shared__ __align__(16) float red[8][16 * kPitch];
@@ -175,12 +192,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const Sk
     const uint16_t* w1 = w + (int64_t)(f0 + gq + 8 < p.F ? gq + 8 : gq) * p.K;
     const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)row0 * p.ldx;
     const int kw = (((p.K + 7) >> 3) + 31) & ~31, kb = warp * kw, ke = min(p.K, kb + kw);
-    if (n <= 8) skinny_sums<BF16, 1>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
-    else if (MAXNB == 2 || (MAXNB > 2 && n <= 16)) skinny_sums<BF16, 2>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
-    else if (MAXNB == 8 && n <= 32) skinny_sums<BF16, 4>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    if (n <= 8) skinny_sums<BF16, 1, LONG>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (MAXNB == 2 || (MAXNB > 2 && n <= 16)) skinny_sums<BF16, 2, LONG>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (MAXNB == 8 && n <= 32) skinny_sums<BF16, 4, LONG>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     // (a decode batch of 48 requests with adapters: 9.9 us, 10.8 as 64 rows; products do not gain)
-    else if (ADAPT && MAXNB == 8 && n <= 48) skinny_sums<BF16, 6>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
-    else if (MAXNB == 8) skinny_sums<BF16, 8>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (ADAPT && MAXNB == 8 && n <= 48) skinny_sums<BF16, 6, LONG>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
+    else if (MAXNB == 8) skinny_sums<BF16, 8, LONG>(w0, w1, x, p.ldx, n, kb, ke, red[warp], kPitch);
     __syncthreads();
     grid_release();  // (late: the next kernel's CTAs then spread over the SMs as evenly as this one's)
     // thread: feature tid % 16, rows tid / 16 + 16 i
@@ -252,15 +269,21 @@ __global__ void __launch_bounds__(kSkinnyThreads, PER_SM) skinny_kernel(const Sk
     }
 }
 
-template <bool BF16, bool OUT32, bool ADAPT>
-static cudaError_t skinny(const SkinnyArgs& p, int rows, dim3 grid, cudaStream_t s) {
-    auto kern = rows <= 8    ? skinny_kernel<BF16, OUT32, ADAPT, 1>
-                : rows <= 16 ? skinny_kernel<BF16, OUT32, ADAPT, 2>
-                             : skinny_kernel<BF16, OUT32, ADAPT, 8>;
+template <bool BF16, bool OUT32, bool ADAPT, bool LONG>
+static cudaError_t skinny_k(const SkinnyArgs& p, int rows, dim3 grid, cudaStream_t s) {
+    auto kern = rows <= 8    ? skinny_kernel<BF16, OUT32, ADAPT, LONG, 1>
+                : rows <= 16 ? skinny_kernel<BF16, OUT32, ADAPT, LONG, 2>
+                             : skinny_kernel<BF16, OUT32, ADAPT, LONG, 8>;
     // at most a CTA an SM (64 rows of one 2048 x 2048 matrix: 6.9 us against 8.7; of 8 matrices, 18.1 against 14.4)
     if constexpr (!ADAPT)
-        if (rows > 16 && grid.x * grid.y <= 148) kern = skinny_kernel<BF16, OUT32, false, 8, 1>;
+        if (rows > 16 && grid.x * grid.y <= 148) kern = skinny_kernel<BF16, OUT32, false, LONG, 8, 1>;
     return launch_behind(kern, grid, kSkinnyThreads, 0, s, p);
+}
+
+template <bool BF16, bool OUT32, bool ADAPT>
+static cudaError_t skinny(const SkinnyArgs& p, int rows, dim3 grid, cudaStream_t s) {
+    return p.K > 8 * kSkinnyPart ? skinny_k<BF16, OUT32, ADAPT, true>(p, rows, grid, s)
+                                 : skinny_k<BF16, OUT32, ADAPT, false>(p, rows, grid, s);
 }
 
 cudaError_t launch_skinny_grouped(const GroupedArgs& g, const void* w, const void* x, int64_t ldx, bool out32,

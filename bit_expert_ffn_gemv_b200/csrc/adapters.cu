@@ -16,6 +16,8 @@
 // of a token's largest value (fp16; adapter.cuh).  The result is rounded once.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "adapter.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -37,6 +39,11 @@ namespace moe {
 // chunk.  8192 tokens of eight requests, K = 2048, x from HBM (5.1 us of it), with
 // an expand_kernel of 8 features behind it: 13 us at rank 16, 15 at 32, 24 at 64.
 constexpr int kShrinkThreads = 256;
+// Values that one MMA accumulator sums (skinny.cu says why).  LONG: a CTA's share of K is
+// more, and so may a warp's be, where five adapters or more share the window; the items
+// of a request's chunk are split over the warps and stay below it.  (The other loop costs
+// the first its registers with small windows: one token 5.4 us without it, 5.75 with.)
+constexpr int kShrinkPart = 512;
 
 // Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K
 // in flight.  Large windows keep theirs in a ring in shared memory, as many as leave
@@ -54,7 +61,7 @@ struct ShrinkCfg {
     static constexpr int kShared = kRing > kRed ? kRing : kRed;  // bytes
 };
 
-template <bool BF16, int WIN, int TERMS, int TILES>
+template <bool BF16, int WIN, int TERMS, int TILES, bool LONG>
 __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const AdapterArgs p) {
     using C = ShrinkCfg<WIN, TILES>;
     extern __shared__ __align__(16) uint8_t shrink_smem[];
@@ -130,56 +137,78 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                     }
                 };
                 auto source = [&](int v) { return v < C::kOctets ? xr[v] : ar[v - C::kOctets]; };
-                if constexpr (C::kRing > 0) {
-                    // a lane copies what it will multiply itself: the ring needs no barrier
-                    uint8_t* ring = shrink_smem + warp * C::kDepth * C::kStep + lane * 16;
-                    auto fetch = [&](uint8_t* to, int k) {
-                        const uint32_t bytes = k + 8 * c < ke ? 16 : 0;
+                // the warp's share of K; IN_PARTS: more than kShrinkPart of it, summed in parts of that many
+                auto walk = [&](auto in_parts) {
+                    constexpr bool IN_PARTS = decltype(in_parts)::value;
+                    float sum[IN_PARTS ? C::kTiles : 1][C::kOctets][4] = {};
+                    auto add = [&](bool last) {
 #pragma unroll
-                        for (int v = 0; v < C::kVecs; ++v)
-                            if (v < octets || v >= C::kOctets) tc::cp16_or_zero(to + v * 512, source(v) + k, bytes);
+                        for (int q = 0; q < C::kTiles; ++q)
+#pragma unroll
+                            for (int o = 0; o < C::kOctets; ++o)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    float& t = sum[IN_PARTS ? q : 0][o][i];
+                                    t += acc[q][o][i];
+                                    acc[q][o][i] = last ? t : 0.f;
+                                }
                     };
+                    if constexpr (C::kRing > 0) {
+                        // a lane copies what it will multiply itself: the ring needs no barrier
+                        uint8_t* ring = shrink_smem + warp * C::kDepth * C::kStep + lane * 16;
+                        auto fetch = [&](uint8_t* to, int k) {
+                            const uint32_t bytes = k + 8 * c < ke ? 16 : 0;
 #pragma unroll
-                    for (int b = 0; b < C::kDepth - 1; ++b) {
-                        if (kb + 32 * b < ke) fetch(ring + b * C::kStep, kb + 32 * b);
-                        tc::cp_commit();
-                    }
-                    int in = C::kDepth - 1, out = 0;  // the ring's places to fill and to read
-                    for (int k = kb; k < ke; k += 32) {
-                        const int ahead = k + 32 * (C::kDepth - 1);
-                        if (ahead < ke) fetch(ring + in * C::kStep, ahead);
-                        tc::cp_commit();
-                        tc::cp_wait<C::kDepth - 1>();
-                        const uint8_t* from = ring + out * C::kStep;
-                        multiply([&](int v) { return *reinterpret_cast<const uint4*>(from + v * 512); });
-                        in = in + 1 == C::kDepth ? 0 : in + 1;
-                        out = out + 1 == C::kDepth ? 0 : out + 1;
-                    }
-                } else {
-                    // (only a last, partial step looks at the end of K)
-                    uint4 held[C::kDepth][C::kVecs];
-                    auto fetch = [&](int b, int k) {
-                        if (k + 32 <= ke) {
+                            for (int v = 0; v < C::kVecs; ++v)
+                                if (v < octets || v >= C::kOctets) tc::cp16_or_zero(to + v * 512, source(v) + k, bytes);
+                        };
 #pragma unroll
-                            for (int v = 0; v < C::kVecs; ++v) held[b][v] = __ldg(reinterpret_cast<const uint4*>(source(v) + k));
-                        } else {
-                            const bool in = k + 8 * c < ke;
-#pragma unroll
-                            for (int v = 0; v < C::kVecs; ++v) held[b][v] = load_or_zero(source(v) + k, in);
+                        for (int b = 0; b < C::kDepth - 1; ++b) {
+                            if (kb + 32 * b < ke) fetch(ring + b * C::kStep, kb + 32 * b);
+                            tc::cp_commit();
                         }
-                    };
+                        int in = C::kDepth - 1, out = 0;  // the ring's places to fill and to read
+                        for (int k = kb; k < ke; k += 32) {
+                            if (IN_PARTS && ((k - kb) & (kShrinkPart - 1)) == 0) add(false);
+                            const int ahead = k + 32 * (C::kDepth - 1);
+                            if (ahead < ke) fetch(ring + in * C::kStep, ahead);
+                            tc::cp_commit();
+                            tc::cp_wait<C::kDepth - 1>();
+                            const uint8_t* from = ring + out * C::kStep;
+                            multiply([&](int v) { return *reinterpret_cast<const uint4*>(from + v * 512); });
+                            in = in + 1 == C::kDepth ? 0 : in + 1;
+                            out = out + 1 == C::kDepth ? 0 : out + 1;
+                        }
+                    } else {
+                        // (only a last, partial step looks at the end of K)
+                        uint4 held[C::kDepth][C::kVecs];
+                        auto fetch = [&](int b, int k) {
+                            if (k + 32 <= ke) {
 #pragma unroll
-                    for (int b = 0; b < C::kDepth - 1; ++b)
-                        if (kb + 32 * b < ke) fetch(b, kb + 32 * b);
-                    for (int k0 = kb; k0 < ke; k0 += 32 * C::kDepth) {
+                                for (int v = 0; v < C::kVecs; ++v) held[b][v] = __ldg(reinterpret_cast<const uint4*>(source(v) + k));
+                            } else {
+                                const bool in = k + 8 * c < ke;
 #pragma unroll
-                        for (int b = 0; b < C::kDepth; ++b) {
-                            const int k = k0 + 32 * b, ahead = k + 32 * (C::kDepth - 1);
-                            if (ahead < ke) fetch((b + C::kDepth - 1) % C::kDepth, ahead);
-                            if (k < ke) multiply([&](int v) { return held[b][v]; });
+                                for (int v = 0; v < C::kVecs; ++v) held[b][v] = load_or_zero(source(v) + k, in);
+                            }
+                        };
+#pragma unroll
+                        for (int b = 0; b < C::kDepth - 1; ++b)
+                            if (kb + 32 * b < ke) fetch(b, kb + 32 * b);
+                        for (int k0 = kb; k0 < ke; k0 += 32 * C::kDepth) {
+                            if (IN_PARTS && ((k0 - kb) & (kShrinkPart - 1)) == 0) add(false);
+#pragma unroll
+                            for (int b = 0; b < C::kDepth; ++b) {
+                                const int k = k0 + 32 * b, ahead = k + 32 * (C::kDepth - 1);
+                                if (ahead < ke) fetch((b + C::kDepth - 1) % C::kDepth, ahead);
+                                if (k < ke) multiply([&](int v) { return held[b][v]; });
+                            }
                         }
                     }
-                }
+                    if (IN_PARTS) add(true);
+                };
+                if (LONG && ke - kb > kShrinkPart) walk(std::bool_constant<LONG>{});
+                else walk(std::false_type{});
             }
             __syncthreads();  // every warp is through with its ring, or the last pass's sums
             float* mr = red + warp * WIN * C::kPitch;
@@ -391,7 +420,8 @@ size_t adapter_workspace(int T, int r) {
 
 template <bool BF16, int WIN, int TERMS, int TILES>
 static cudaError_t shrink_tiles(const AdapterArgs& p, cudaStream_t s) {
-    auto kern = shrink_kernel<BF16, WIN, TERMS, TILES>;
+    auto kern = (p.K + p.slices - 1) / p.slices > kShrinkPart ? shrink_kernel<BF16, WIN, TERMS, TILES, true>
+                                                              : shrink_kernel<BF16, WIN, TERMS, TILES, false>;
     const int smem = ShrinkCfg<WIN, TILES>::kShared + WIN * p.r * 4;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

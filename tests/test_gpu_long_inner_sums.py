@@ -48,3 +48,24 @@ def test_projection_of_few_tokens(T, dtype):
                               ids, w=w, flags=moe.MOE_OUT_FP32)
     ref = x.double() @ w.double().T
     assert float(((got.double() - ref) / ref).abs().max()) <= _bound(K)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,K,ids", [(1, 1 << 17, "one"), (9, 1 << 17, "one"), (9, 1 << 17, "mixed"), (100, 40008, "mixed"),
+                                     (100, 40008, "one"), (1300, 16392, "one"), (1300, 16392, "mixed"), (8200, 4104, "mixed"),
+                                     (8200, 4104, "one")])
+@pytest.mark.parametrize("r", [8, 32, 72])
+def test_inner_values(r, T, K, ids, dtype):
+    """v itself, by a B that is the identity: every token's own values, at each window, rank pass and share of K."""
+    L = 9
+    x, a = _positive((T, K), dtype, 5), _positive((L, r, K), dtype, 6)
+    b = torch.eye(r, device="cuda").to(dtype).expand(L, r, r).contiguous()
+    at = (torch.arange(T, device="cuda") % L if ids == "mixed" else torch.full((T,), 4, device="cuda")).int()
+    scale = torch.full((L,), 2.0 ** -6, device="cuda")  # (v below 2^15: fp16 keeps 22 bits of it)
+    got = moe.adapter_project(x, a, b, at, scale=scale, flags=moe.MOE_OUT_FP32)
+    ref = torch.zeros(T, r, dtype=torch.float64, device="cuda")
+    for i in range(L):
+        m = (at == i).nonzero()[:, 0]
+        ref[m] = 2.0 ** -6 * x[m].double() @ a[i].double().T
+    # fp16: two terms hold 2^-23 of the token's largest value, at most four times the smallest here
+    assert float(((got.double() - ref) / ref).abs().max()) <= _bound(K) + (2.0 ** -21 if dtype == torch.float16 else 2.0 ** -24)

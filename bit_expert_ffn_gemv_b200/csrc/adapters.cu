@@ -40,9 +40,8 @@ namespace moe {
 // an expand_kernel of 8 features behind it: 13 us at rank 16, 15 at 32, 24 at 64.
 constexpr int kShrinkThreads = 256;
 // Values that one MMA accumulator sums (skinny.cu says why).  LONG: a CTA's share of K is
-// more, and so may a warp's be, where five adapters or more share the window; the items
-// of a request's chunk are split over the warps and stay below it.  (The other loop costs
-// the first its registers with small windows: one token 5.4 us without it, 5.75 with.)
+// more, and so may a warp's be, where adapters mix in the window; the items of a request's
+// chunk are split over the warps and stay below it up to K = 4096.
 constexpr int kShrinkPart = 512;
 
 // Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K
@@ -207,7 +206,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                     }
                     if (IN_PARTS) add(true);
                 };
-                if (LONG && ke - kb > kShrinkPart) walk(std::bool_constant<LONG>{});
+                // (both loops in one kernel only with large windows, whose chunks of a request stay below a part: with
+                // small ones they spill, 1000 mixed tokens of rank 64, K = 4096: 154 us against 76)
+                if (LONG && (WIN == 8 || ke - kb > kShrinkPart)) walk(std::bool_constant<LONG>{});
                 else walk(std::false_type{});
             }
             __syncthreads();  // every warp is through with its ring, or the last pass's sums

@@ -158,7 +158,8 @@ moe_status moe_adapter_check(const moe_adapter_args* args, uint32_t flags) {
     if (q.tokens == 0) return MOE_OK;
     if (!good(q.x) || !good(q.a) || !good(q.b) || !good(q.y) || !good(q.workspace) || (q.w && !aligned16(q.w)) ||
         !q.ids || !aligned4(q.ids) || !aligned4(q.scale) ||
-        q.workspace_bytes < moe_adapter_workspace(q.tokens, q.rank) || q.x == q.y)
+        q.workspace_bytes < moe_adapter_workspace(q.tokens, q.rank) || q.y == q.x || q.y == q.w || q.y == q.a ||
+        q.y == q.b || q.y == q.workspace || q.workspace == q.x)
         return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }

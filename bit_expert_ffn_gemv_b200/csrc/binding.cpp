@@ -387,7 +387,8 @@ PyObject* adapter_beside(PyObject*, PyObject* const* a, Py_ssize_t count) {
                       "x: a contiguous [T, ", d, "] bf16 tensor is expected, not ", c.x.t.sizes(), " of ", c.x.t.scalar_type());
     TORCH_CHECK_VALUE(p.n == d, "b: ", d, " features are expected, not ", p.n);
     p.ldy = d;
-    p.y = p.workspace = reinterpret_cast<void*>(16);  // (to be allocated: aligned)
+    p.y = reinterpret_cast<void*>(16);  // (these two are allocated later: aligned)
+    p.workspace = reinterpret_cast<void*>(32);
     if (a[5] != Py_None) {
         const Tensor& y = tensor(a[5], "y");
         block(y, "y", c.x.dev, c.type, {c.x.rows, d});

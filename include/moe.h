@@ -499,9 +499,9 @@ typedef struct {
 size_t moe_adapter_workspace(int32_t tokens, int32_t rank);
 
 /*
- * x and y must not overlap.  Errors: INVALID_ARG (a field out of the ranges
- * above, a short pitch or workspace, NULL or misaligned pointer, y == x,
- * unknown flag), CUDA.
+ * y and the workspace overlap no operand.  Errors: INVALID_ARG (a field out of
+ * the ranges above, a short pitch or workspace, NULL or misaligned pointer, y or
+ * the workspace an operand, unknown flag), CUDA.
  */
 moe_status moe_adapter_project(const moe_adapter_args* args, uint32_t flags, void* stream);
 

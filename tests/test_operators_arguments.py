@@ -60,9 +60,21 @@ def test_adapter_check():
     """moe_adapter_check is moe_adapter_project's refusals, without the call."""
     import ctypes
     good = dict(x=P, ldx=64, tokens=10, n=32, k=64, w=0, a=P, b=P, scale=0, ids=P, n_adapters=3, rank=16, y=2 * P, ldy=32,
-                workspace=P, workspace_bytes=1 << 20)
+                workspace=3 * P, workspace_bytes=1 << 20)
     check = moe.lib().moe_adapter_check
     assert check(ctypes.byref(moe.MoeAdapterArgs(**good)), 0x3) == 0
     assert check(None, 0) == 1 and check(ctypes.byref(moe.MoeAdapterArgs(**good)), 0x4) == 1
     for bad in (dict(rank=12), dict(y=P), dict(a=P + 8), dict(ids=0), dict(n=4), dict(ldy=24), dict(workspace_bytes=8)):
         assert check(ctypes.byref(moe.MoeAdapterArgs(**dict(good, **bad))), 0) == 1
+
+
+@pytest.mark.parametrize("bad", [dict(w=2 * P), dict(a=2 * P), dict(b=2 * P), dict(x=2 * P), dict(workspace=2 * P), dict(workspace=P)],
+                         ids=str)
+def test_adapters_over_an_operand(bad):
+    """y is 2 P and x P: neither y nor the workspace may be an operand."""
+    import ctypes
+    good = dict(x=P, ldx=64, tokens=10, n=32, k=64, w=3 * P, a=4 * P, b=5 * P, scale=0, ids=P, n_adapters=3, rank=16, y=2 * P,
+                ldy=32, workspace=6 * P, workspace_bytes=1 << 20)
+    assert moe.lib().moe_adapter_check(ctypes.byref(moe.MoeAdapterArgs(**good)), 0) == 0
+    assert moe.lib().moe_adapter_check(ctypes.byref(moe.MoeAdapterArgs(**dict(good, **bad))), 0) == 1
+    assert moe.lib().moe_adapter_project(ctypes.byref(moe.MoeAdapterArgs(**dict(good, **bad))), 0, None) == 1

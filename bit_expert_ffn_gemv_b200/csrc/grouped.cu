@@ -46,6 +46,7 @@
 #include "adapter.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "pack16.cuh"
 #include "tc.cuh"
 
 namespace moe {
@@ -80,17 +81,7 @@ struct GroupedMaps {
 };
 
 // 16-bit pair in the requested type
-MOE_DEV uint32_t pack16(float lo, float hi, bool bf16) {
-    if (bf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-MOE_DEV uint16_t to16(float v, bool bf16) {
-    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
+MOE_DEV uint32_t pack16(float lo, float hi, bool bf16) { return bf16 ? pack2<true>(lo, hi) : pack2<false>(lo, hi); }
 
 struct GroupedTile {
     int e, row0, n;  // group; first row and rows of the tile (weights: of the group)

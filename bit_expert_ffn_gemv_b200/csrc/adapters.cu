@@ -37,7 +37,7 @@ namespace moe {
 // with fewer items several warps share one and split its K.  Bound by the A
 // rows of a decode batch (every token another adapter) or the x of a prefill
 // chunk.  8192 tokens of eight requests, K = 2048, x from HBM (5.1 us of it), with
-// an expand_kernel of 8 features behind it: 13 us at rank 16, 15 at 32, 24 at 64.
+// an expand_kernel of 8 features behind it: 15 us at rank 16, 17 at 32, 27 at 64.
 constexpr int kShrinkThreads = 256;
 // Values that one MMA accumulator sums (skinny.cu says why).  LONG: a CTA's share of K is
 // more, and so may a warp's be, where adapters mix in the window; the items of a request's
@@ -46,10 +46,10 @@ constexpr int kShrinkPart = 512;
 
 // Octets of tokens per item, 16-row tiles of A per pass, and the steps of 32 of K
 // in flight.  Large windows keep theirs in a ring in shared memory, as many as leave
-// room for two CTAs an SM (8192 tokens of rank 32 and K = 2048, x from HBM: 15.1 us with
-// the ring, 16.1 with registers; of mixed adapters 46 against 72); small ones hold them
-// in registers, as many as about 50 hold (512 tokens of 30 adapters beside a
-// projection: 36 us, 40 with a ring).
+// room for two CTAs an SM (8192 tokens of rank 32 and K = 2048, x from HBM, v in two
+// terms: 15.1 us with the ring, 16.1 with registers; of mixed adapters 46 against 72);
+// small ones hold them in registers, as many as about 50 hold (512 tokens of 30
+// adapters beside a projection, v in two terms: 36 us, 40 with a ring; in three 38).
 template <int WIN, int TILES>
 struct ShrinkCfg {
     static constexpr int kOctets = WIN / 8, kTiles = TILES, kRows = 16 * TILES, kPitch = kRows + 4;
@@ -118,48 +118,52 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
 #pragma unroll
                 for (int q = 0; q < 2 * C::kTiles; ++q)
                     ar[q] = A + ((int64_t)a * p.r + j0 + (q * 8 + gq < rows ? q * 8 + gq : gq)) * p.K + 8 * c;
-                auto multiply = [&](auto operand) {
-                    uint4 bv[C::kOctets];
+                // The warp's share of K.  IN_PARTS: more than kShrinkPart of it, summed in parts of that many, the item's
+                // octets (of which a window of many adapters has one each) one after the other, o0 first to last
+                auto walk = [&](auto in_parts, int o0) {
+                    constexpr bool IN_PARTS = decltype(in_parts)::value;
+                    constexpr int OCT = IN_PARTS ? 1 : C::kOctets;
+                    float now[C::kTiles][OCT][4] = {}, before[C::kTiles][OCT][4] = {};
+                    const uint16_t* xs[OCT];
 #pragma unroll
                     for (int o = 0; o < C::kOctets; ++o)
-                        if (o == 0 || o < octets) bv[o] = operand(o);
+                        if (!IN_PARTS || o == o0) xs[IN_PARTS ? 0 : o] = xr[o];
+                    auto source = [&](int v) { return v < OCT ? xs[v] : ar[v - OCT]; };
+                    auto multiply = [&](auto operand) {
+                        uint4 bv[OCT];
 #pragma unroll
-                    for (int q = 0; q < C::kTiles; ++q) {
-                        const uint4 lo = operand(C::kOctets + 2 * q), hi = operand(C::kOctets + 2 * q + 1);
-                        const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
+                        for (int o = 0; o < OCT; ++o)
+                            if (o == 0 || o < octets) bv[o] = operand(o);
 #pragma unroll
-                        for (int o = 0; o < C::kOctets; ++o) {
-                            if (o > 0 && o >= octets) break;
-                            mma16<BF16>(acc[q][o], f0, bv[o].x, bv[o].y);
-                            mma16<BF16>(acc[q][o], f1, bv[o].z, bv[o].w);
+                        for (int q = 0; q < C::kTiles; ++q) {
+                            const uint4 lo = operand(OCT + 2 * q), hi = operand(OCT + 2 * q + 1);
+                            const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+                            for (int o = 0; o < OCT; ++o) {
+                                if (o > 0 && o >= octets) break;
+                                mma16<BF16>(now[q][o], f0, bv[o].x, bv[o].y);
+                                mma16<BF16>(now[q][o], f1, bv[o].z, bv[o].w);
+                            }
                         }
-                    }
-                };
-                auto source = [&](int v) { return v < C::kOctets ? xr[v] : ar[v - C::kOctets]; };
-                // the warp's share of K; IN_PARTS: more than kShrinkPart of it, summed in parts of that many
-                auto walk = [&](auto in_parts) {
-                    constexpr bool IN_PARTS = decltype(in_parts)::value;
-                    float sum[IN_PARTS ? C::kTiles : 1][C::kOctets][4] = {};
-                    auto add = [&](bool last) {
+                    };
+                    auto end_part = [&] {
 #pragma unroll
                         for (int q = 0; q < C::kTiles; ++q)
 #pragma unroll
-                            for (int o = 0; o < C::kOctets; ++o)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    float& t = sum[IN_PARTS ? q : 0][o][i];
-                                    t += acc[q][o][i];
-                                    acc[q][o][i] = last ? t : 0.f;
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                before[q][0][i] += now[q][0][i];
+                                now[q][0][i] = 0.f;
+                            }
                     };
+                    constexpr int VECS = OCT + 2 * C::kTiles;
                     if constexpr (C::kRing > 0) {
                         // a lane copies what it will multiply itself: the ring needs no barrier
                         uint8_t* ring = shrink_smem + warp * C::kDepth * C::kStep + lane * 16;
                         auto fetch = [&](uint8_t* to, int k) {
                             const uint32_t bytes = k + 8 * c < ke ? 16 : 0;
 #pragma unroll
-                            for (int v = 0; v < C::kVecs; ++v)
-                                if (v < octets || v >= C::kOctets) tc::cp16_or_zero(to + v * 512, source(v) + k, bytes);
+                            for (int v = 0; v < VECS; ++v)
+                                if (v == 0 || v < octets || v >= OCT) tc::cp16_or_zero(to + v * 512, source(v) + k, bytes);
                         };
 #pragma unroll
                         for (int b = 0; b < C::kDepth - 1; ++b) {
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                         }
                         int in = C::kDepth - 1, out = 0;  // the ring's places to fill and to read
                         for (int k = kb; k < ke; k += 32) {
-                            if (IN_PARTS && ((k - kb) & (kShrinkPart - 1)) == 0) add(false);
+                            if (IN_PARTS && ((k - kb) & (kShrinkPart - 1)) == 0) end_part();
                             const int ahead = k + 32 * (C::kDepth - 1);
                             if (ahead < ke) fetch(ring + in * C::kStep, ahead);
                             tc::cp_commit();
@@ -180,22 +184,22 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                         }
                     } else {
                         // (only a last, partial step looks at the end of K)
-                        uint4 held[C::kDepth][C::kVecs];
+                        uint4 held[C::kDepth][VECS];
                         auto fetch = [&](int b, int k) {
                             if (k + 32 <= ke) {
 #pragma unroll
-                                for (int v = 0; v < C::kVecs; ++v) held[b][v] = __ldg(reinterpret_cast<const uint4*>(source(v) + k));
+                                for (int v = 0; v < VECS; ++v) held[b][v] = __ldg(reinterpret_cast<const uint4*>(source(v) + k));
                             } else {
                                 const bool in = k + 8 * c < ke;
 #pragma unroll
-                                for (int v = 0; v < C::kVecs; ++v) held[b][v] = load_or_zero(source(v) + k, in);
+                                for (int v = 0; v < VECS; ++v) held[b][v] = load_or_zero(source(v) + k, in);
                             }
                         };
 #pragma unroll
                         for (int b = 0; b < C::kDepth - 1; ++b)
                             if (kb + 32 * b < ke) fetch(b, kb + 32 * b);
                         for (int k0 = kb; k0 < ke; k0 += 32 * C::kDepth) {
-                            if (IN_PARTS && ((k0 - kb) & (kShrinkPart - 1)) == 0) add(false);
+                            if (IN_PARTS && ((k0 - kb) & (kShrinkPart - 1)) == 0) end_part();
 #pragma unroll
                             for (int b = 0; b < C::kDepth; ++b) {
                                 const int k = k0 + 32 * b, ahead = k + 32 * (C::kDepth - 1);
@@ -204,12 +208,29 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const Adapter
                             }
                         }
                     }
-                    if (IN_PARTS) add(true);
+#pragma unroll
+                    for (int o = 0; o < C::kOctets; ++o) {
+                        if (IN_PARTS && o != o0) continue;
+#pragma unroll
+                        for (int q = 0; q < C::kTiles; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int own = IN_PARTS ? 0 : o;
+                                acc[q][o][i] = IN_PARTS ? before[q][own][i] + now[q][own][i] : now[q][own][i];
+                            }
+                    }
                 };
                 // (both loops in one kernel only with large windows, whose chunks of a request stay below a part: with
                 // small ones they spill, 1000 mixed tokens of rank 64, K = 4096: 154 us against 76)
-                if (LONG && (WIN == 8 || ke - kb > kShrinkPart)) walk(std::bool_constant<LONG>{});
-                else walk(std::false_type{});
+                if constexpr (LONG && WIN == 8) {
+                    walk(std::true_type{}, 0);
+                } else if constexpr (LONG) {
+                    if (ke - kb > kShrinkPart)
+                        for (int o = 0; o < octets; ++o) walk(std::true_type{}, o);
+                    else walk(std::false_type{}, 0);
+                } else {
+                    walk(std::false_type{}, 0);
+                }
             }
             __syncthreads();  // every warp is through with its ring, or the last pass's sums
             float* mr = red + warp * WIN * C::kPitch;
@@ -400,8 +421,8 @@ __global__ void __launch_bounds__(128) expand_kernel(const AdapterArgs p) {
 // ---------------------------------------------------------------- launcher
 // A window is 8 tokens while such windows fit the 148 SMs once, else 32.  Small
 // windows share a mixed batch's A rows out over more CTAs (512 tokens of 30
-// adapters, rank 16: 22 us against 29), large ones read the A rows of a long
-// run less often (8192 tokens of one adapter, rank 64: 25 us against 39).
+// adapters, rank 16, v in two terms: 22 us against 29), large ones read the A rows of a long
+// run less often (8192 tokens of one adapter, rank 64, v in two terms: 25 us against 39).
 constexpr int kSmallWindowTokens = 148 * 8;
 
 // CTAs that split a window's K: a power of two up to 8, so that the windows'

@@ -36,10 +36,16 @@
 // core's rate under the 1000 W cap (64 even groups of 640 rows by 2048 x 768:
 // 140 us, a batched library product 140; their weights' gradient at 1536 x 2048:
 // 231 to 267 us against 247).  Small groups are bound by reading the matrices:
-// 640 rows over 512 experts of 1536 x 2048 take 190 us, 5.9 TB/s or 90% of the
-// measured copy; 81920 rows over 512 even ones 590 us, 98% of it.  Below about
-// 10 us a call is its start-up: offsets, tensor memory, the cluster's barrier
-// and the first load, 3 us each way.
+// 64 tokens' 640 rows over 512 experts of 1536 x 2048 (some 204 in use, 1.29 GB)
+// take 190 us, the measured copy's rate; 81920 rows over 512 even ones 590 us, 98%
+// of it.  Below about 10 us a call is its start-up: offsets, tensor memory, the
+// cluster's barrier and the first load, 3 us each way with up to 64 groups.  Sorting
+// the groups by cost compares all pairs of them and grows with their square: the
+// weights' gradient of 64 x 64 matrices, two rows a group, takes 5.6 us for 16
+// groups, 11 for 128, 49 for 512 and 135 for 1024, a product of 256 rows a group
+// 18 us for 64, 36 for 256, 112 for 512 and 326 for 1024 (products of fewer rows a
+// group are not sorted: 14 and 25 us for 512 and 1024).  A group's contraction is
+// never split: one of 40003 rows by 256 x 256 takes 187 us on one pair of SMs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -7,8 +7,10 @@
 // shared memory sits between HBM and the tensor core and no padded row tile is
 // computed.  The warps' sums meet in shared memory in warp order
 // (deterministic).  Bound by HBM, 2 N K bytes per matrix, and by the latency of
-// a CTA's few loads: ten rows of ten 1536 x 2048 matrices take 13.5 us, 71% of
-// the measured copy; one row-block of 64 rows by 2048 x 2048 6.9 us.
+// a CTA's few loads: ten rows of ten 1536 x 2048 matrices take 13.8 us, 70% of
+// the measured copy; one row-block of 64 rows by 2048 x 2048 6.9 us.  With 17 to
+// 64 rows and two CTAs an SM the eight row blocks do not fit 128 registers: 300
+// bytes a thread are read back from local memory (8 matrices by 64 rows 14.5 us).
 //
 // Grouped form: a CTA finds the group it works for in the offsets (one round of
 // loads and a prefix count of those that hold rows), so no list of groups is
